@@ -18,7 +18,15 @@ Shapes follow the C header (bf16 unless stated; every shape is checked before th
   dsa_decode(q [B,Hq,128], qI [B,HI,64], w [B,HI], k_new/v_new [B,Hkv,128], kI_new [B,64],
              k_cache/v_cache [B,Lmax,Hkv,128], kI_cache [B,Lmax,64], ctx_len int32 [B], topk, scale,
              out [B,Hq,128], idx_out int32 [B,topk] = None, ws=None, update_ctx=False)
-Every tensor must be contiguous and on the current CUDA device.
+  dsa_rope(x [T,H,D] bf16 or fp32, out [T,H,D], inv_freq fp64 [R/2], pos int32 [T] = None, pos0=0,
+           rot_offset=0, interleaved=False, mscale=1.0, inverse=False)      (x, out: strides free)
+  dsa_kv_append(k_new/v_new [N,Hkv,128] (strides free), k_pages/v_pages float8_e4m3fn or int8
+                [pages,page,Hkv,128], k_scale/v_scale fp32 [pages,Hkv], page_table int32 [B,max_pages],
+                ctx_len int32 [B], cu_new int32 [B+1] = None, inv_freq fp64 [R/2] = None,
+                rope_pos int32 [N] = None, rot_offset=0, interleaved=False, mscale=1.0)
+  dsa_paged_attn(q [T,Hq,128], k_pages, v_pages, k_scale, v_scale, page_table, n_keys int32 [T], scale,
+                 out [T,Hq,128], seq int32 [T] = None, idx int32 [T,topk] = None, lse fp32 [T,Hq] = None, ws=None)
+Every tensor must be on the current CUDA device, and contiguous where "strides free" does not stand.
 """
 from __future__ import annotations
 
@@ -38,10 +46,17 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE, DSA_ERR_CUDA, DSA_ERR_TIMEOUT, \
     DSA_ERR_DEVICE_INPUT = range(7)
-DSA_OP_INDEX, DSA_OP_TOPK, DSA_OP_SPARSE_ATTN, DSA_OP_PREFILL, DSA_OP_DECODE, DSA_OP_INDEXER_KL = range(6)
-PROFILE_KINDS = ("indexer", "topk", "sparse_attn", "combine", "decode_append", "advance", "selftest", "kl")
+DSA_OP_INDEX, DSA_OP_TOPK, DSA_OP_SPARSE_ATTN, DSA_OP_PREFILL, DSA_OP_DECODE, DSA_OP_INDEXER_KL, \
+    DSA_OP_PAGED_ATTN = range(7)
+DSA_BF16, DSA_FP32 = range(2)
+DSA_ROPE_HALF, DSA_ROPE_INTERLEAVED = range(2)
+DSA_KV_E4M3, DSA_KV_INT8 = range(2)
+ROPE_SCALINGS = ("plain", "linear", "ntk", "yarn")
+PROFILE_KINDS = ("indexer", "topk", "sparse_attn", "combine", "decode_append", "advance", "selftest", "kl", "rope",
+                 "kv_append", "paged_attn")
 
 _p, _i, _i64, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+_d = ctypes.c_double
 _SIGS = {
     "dsa_status_string": (ctypes.c_char_p, [_i]),
     "dsa_version": (_i, []),
@@ -61,6 +76,12 @@ _SIGS = {
                                 _p, _p, _p]),
     "dsa_decode_noalloc_scratch_bytes": (_sz, []),
     "dsa_indexer_kl": (_i, [_p, _p, _p, _p, _p, _i64, _i, _i, _i, _i, _i, _f, _p, _p, _sz, _p]),
+    "dsa_rope": (_i, [_p, _i, _i64, _i, _i, _i64, _i64, _p, _i64, _p, _i, _i, _i, _f, _i, _p, _i64, _i64, _p]),
+    "dsa_rope_freqs": (_i, [_i, _d, _i, _d, _d, _d, _d, _p, _p]),
+    "dsa_kv_append": (_i, [_p, _p, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _i, _i, _i, _f, _i, _p, _p, _p, _p,
+                           _p, _i, _i, _i, _i, _i, _i, _p]),
+    "dsa_paged_attn": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _p, _p,
+                            _p, _sz, _p]),
     "dsa_workspace_size": (_sz, [_i, _i64, _i, _i, _i, _i]),
     "dsa_sync_status": (_i, [_p]),
     "dsa_error_site": (ctypes.c_uint, []),
@@ -322,6 +343,138 @@ def dsa_decode(q, qI, w, k_new, v_new, kI_new, k_cache, v_cache, kI_cache, ctx_l
                          float(scale), int(bool(update_ctx)), _ptr(out), _ptr(idx_out), _ptr(ws), _nbytes(ws),
                          _stream(stream))
     _check(st, "dsa_decode")
+
+
+def _heads(t, dtype, name, shape):
+    """A [tokens, heads, dims] operand whose tokens and heads may lie any distance apart: checks it like
+    _need and returns its strides between tokens and heads (those of an axis of one entry are free)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or any(e is not None and int(e) != n for e, n in zip(shape, t.shape)):
+        want = ", ".join("*" if e is None else str(int(e)) for e in shape)
+        raise ValueError(f"{name} must have shape [{want}], got {list(t.shape)}")
+    T, H, D = t.shape
+    ts, hs, ds = t.stride()
+    if ds != 1 and D != 1:
+        raise ValueError(f"{name}'s last axis must be contiguous")
+    if H == 1:
+        hs = (D + 7) // 8 * 8
+    if T == 1:
+        ts = H * hs
+    return ts, hs
+
+
+def rope_freqs(rot_dim: int, theta: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+               orig_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(frequencies, mscale) for dsa_rope and dsa_kv_append: a float64 CPU tensor [rot_dim / 2], to be moved
+    to the GPU once, and the factor that goes with them; scaling is one of ROPE_SCALINGS."""
+    import torch
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {ROPE_SCALINGS}, got {scaling!r}")
+    f = torch.empty(max(0, int(rot_dim)) // 2, dtype=torch.float64)
+    m = ctypes.c_float()
+    _check(_lib.dsa_rope_freqs(int(rot_dim), float(theta), ROPE_SCALINGS.index(scaling), float(factor),
+                               float(orig_len), float(beta_fast), float(beta_slow), _ptr(f),
+                               ctypes.cast(ctypes.byref(m), ctypes.c_void_p)), "dsa_rope_freqs")
+    return f, m.value
+
+
+def dsa_rope(x, out, inv_freq, pos=None, pos0: int = 0, rot_offset: int = 0, interleaved: bool = False,
+             mscale: float = 1.0, inverse: bool = False, stream=None) -> None:
+    """Rotary positions of x's heads into out (which may be x); inverse gives the gradient of the same."""
+    import torch
+    if getattr(x, "dtype", None) not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x must be a bfloat16 or float32 tensor, got {getattr(x, 'dtype', type(x))}")
+    x_ts, x_hs = _heads(x, x.dtype, "x", (None, None, None))
+    T, H, D = x.shape
+    out_ts, out_hs = _heads(out, x.dtype, "out", (T, H, D))
+    _need(inv_freq, torch.float64, "inv_freq", (None,))
+    if pos is not None:
+        _need(pos, torch.int32, "pos", (T,))
+    _on_device(x=x, out=out, inv_freq=inv_freq, pos=pos)
+    st = _lib.dsa_rope(_ptr(x), DSA_BF16 if x.dtype == torch.bfloat16 else DSA_FP32, T, H, D, x_ts, x_hs, _ptr(pos),
+                       pos0, _ptr(inv_freq), rot_offset, 2 * inv_freq.shape[0], int(bool(interleaved)), float(mscale),
+                       int(bool(inverse)), _ptr(out), out_ts, out_hs, _stream(stream))
+    _check(st, "dsa_rope")
+
+
+def _cache_operands(k_pages, v_pages, k_scale, v_scale, page_table):
+    """Format and sizes of a paged cache: (kv_format, num_pages, page_size, Hkv, D, B, max_pages)."""
+    import torch
+    formats = {torch.float8_e4m3fn: DSA_KV_E4M3, torch.int8: DSA_KV_INT8}
+    if getattr(k_pages, "dtype", None) not in formats:
+        raise TypeError(f"k_pages must be a float8_e4m3fn or int8 tensor, got {getattr(k_pages, 'dtype', type(k_pages))}")
+    _need(k_pages, k_pages.dtype, "k_pages", (None, None, None, None))
+    num_pages, page, Hkv, D = k_pages.shape
+    _need(v_pages, k_pages.dtype, "v_pages", k_pages.shape)
+    _need(k_scale, torch.float32, "k_scale", (num_pages, Hkv))
+    _need(v_scale, torch.float32, "v_scale", (num_pages, Hkv))
+    _need(page_table, torch.int32, "page_table", (None, None))
+    return formats[k_pages.dtype], num_pages, page, Hkv, D, page_table.shape[0], page_table.shape[1]
+
+
+def dsa_kv_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, page_table, ctx_len, cu_new=None, inv_freq=None,
+                  rope_pos=None, rot_offset: int = 0, interleaved: bool = False, mscale: float = 1.0,
+                  stream=None) -> None:
+    """Append tokens to a paged 8-bit cache at positions ctx_len[b].., keys rotated where inv_freq is given."""
+    import torch
+    fmt, num_pages, page, Hkv, D, B, max_pages = _cache_operands(k_pages, v_pages, k_scale, v_scale, page_table)
+    k_ts, k_hs = _heads(k_new, torch.bfloat16, "k_new", (None, Hkv, D))
+    N = k_new.shape[0]
+    v_ts, v_hs = _heads(v_new, torch.bfloat16, "v_new", (N, Hkv, D))
+    _need(ctx_len, torch.int32, "ctx_len", (B,))
+    if cu_new is not None:
+        _need(cu_new, torch.int32, "cu_new", (B + 1,))
+    elif N != B:
+        raise ValueError(f"k_new must have one token for each of page_table's {B} sequences where cu_new is not given, "
+                         f"got {N}")
+    if inv_freq is not None:
+        _need(inv_freq, torch.float64, "inv_freq", (None,))
+    if rope_pos is not None:
+        _need(rope_pos, torch.int32, "rope_pos", (N,))
+    _on_device(k_new=k_new, v_new=v_new, k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale,
+               page_table=page_table, ctx_len=ctx_len, cu_new=cu_new, inv_freq=inv_freq, rope_pos=rope_pos)
+    st = _lib.dsa_kv_append(_ptr(k_new), _ptr(v_new), k_ts, k_hs, v_ts, v_hs, N, _ptr(cu_new), _ptr(ctx_len),
+                            _ptr(rope_pos), _ptr(inv_freq), rot_offset,
+                            0 if inv_freq is None else 2 * inv_freq.shape[0], int(bool(interleaved)), float(mscale), fmt,
+                            _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), B, num_pages,
+                            page, max_pages, Hkv, D, _stream(stream))
+    _check(st, "dsa_kv_append")
+
+
+def dsa_paged_attn(q, k_pages, v_pages, k_scale, v_scale, page_table, n_keys, scale: float, out, seq=None, idx=None,
+                   lse=None, ws=None, stream=None) -> None:
+    """Attention of q's rows over a paged 8-bit cache: the first n_keys[t] keys of each row's sequence, or
+    those of them that idx names."""
+    import torch
+    bf = torch.bfloat16
+    fmt, num_pages, page, Hkv, D, B, max_pages = _cache_operands(k_pages, v_pages, k_scale, v_scale, page_table)
+    _need(q, bf, "q", (None, None, D))
+    T, Hq = q.shape[0], q.shape[1]
+    _need(out, bf, "out", (T, Hq, D)), _need(n_keys, torch.int32, "n_keys", (T,))
+    if seq is not None:
+        _need(seq, torch.int32, "seq", (T,))
+    elif T != B:
+        raise ValueError(f"q must have one row for each of page_table's {B} sequences where seq is not given, got {T}")
+    if idx is not None:
+        _need(idx, torch.int32, "idx", (T, None))
+    if lse is not None:
+        _need(lse, torch.float32, "lse", (T, Hq))
+    _on_device(q=q, k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
+               n_keys=n_keys, out=out, seq=seq, idx=idx, lse=lse, ws=ws)
+    if ws is None and stream is not None:
+        with torch.cuda.stream(stream):  # memory that is in order with the kernels' stream
+            ws = _workspace(None, DSA_OP_PAGED_ATTN, 1, T, Hq, 1, 1, q)
+    else:
+        ws = _workspace(ws, DSA_OP_PAGED_ATTN, 1, T, Hq, 1, 1, q)
+    st = _lib.dsa_paged_attn(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+                             _ptr(seq), _ptr(n_keys), _ptr(idx), fmt, T, B, num_pages, page, max_pages, Hq, Hkv, D,
+                             0 if idx is None else idx.shape[1], float(scale), _ptr(out), _ptr(lse), _ptr(ws),
+                             _nbytes(ws), _stream(stream))
+    _check(st, "dsa_paged_attn")
 
 
 def sync_status(stream=None) -> int:

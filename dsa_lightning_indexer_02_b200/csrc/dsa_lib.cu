@@ -1,11 +1,12 @@
 // libdsa.so: the C ABI declared in include/dsa.h.  Host side: argument validation, workspace
 // carving, TMA descriptor encoding, launch configuration and the fused prefill/decode drivers.
-// Every computation of the path runs in the kernels of indexer.cuh, topk.cuh and attn.cuh.
+// Every computation of the path runs in the kernels of the .cuh files beside this one.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -16,7 +17,10 @@
 #include "kl.cuh"
 #include "dsa.h"
 #include "indexer.cuh"
+#include "kv8.cuh"
+#include "paged_attn.cuh"
 #include "ptx.cuh"
+#include "rope.cuh"
 #include "topk.cuh"
 
 using namespace dsa;
@@ -74,7 +78,8 @@ struct LaunchScope {
     }
 };
 
-enum { K_INDEX = 0, K_TOPK = 1, K_ATTN = 2, K_COMBINE = 3, K_APPEND = 4, K_ADVANCE = 5, K_SELFTEST = 6, K_KL = 7 };
+enum { K_INDEX = 0, K_TOPK = 1, K_ATTN = 2, K_COMBINE = 3, K_APPEND = 4, K_ADVANCE = 5, K_SELFTEST = 6, K_KL = 7, K_ROPE = 8,
+       K_KV_APPEND = 9, K_PAGED_ATTN = 10 };
 
 dsa_status launch_status() {
     cudaError_t e = cudaGetLastError();
@@ -464,6 +469,66 @@ dsa_status run_attn(const AttnParams& P, cudaStream_t s) {
     return launch_attn_t<2>(P, s);
 }
 
+// ------------------------------------------------------------------ rotary positions
+// Whether [T, H, D] rows with these strides keep clear of one another.
+bool rows_disjoint(int64_t T, int H, int D, int64_t ts, int64_t hs) {
+    if (T == 1) return H == 1 || hs >= D;
+    if (H == 1) return ts >= D;
+    return (hs >= D && ts >= (H - 1) * hs + D) || (ts >= D && hs >= (T - 1) * ts + D);
+}
+
+dsa_status run_rope(const void* x, int dtype, int64_t T, int H, int D, RopeParams P, bool in_place, bool inter,
+                    cudaStream_t s) {
+    const int V = dtype == DSA_BF16 ? 8 : 4;
+    P.x = x, P.T = T, P.H = H;
+    P.rot_units = P.n / V;
+    P.copy_vecs = in_place ? 0 : (D - 2 * P.n) / V;
+    P.units = P.rot_units + (P.copy_vecs + 1) / 2;
+    // a block: whole tokens where they fit, as many heads of one otherwise
+    P.head_slots = std::min(H, std::max(1, kRopeThreads / P.units));
+    P.tokens = std::max(1, kRopeThreads / (P.units * P.head_slots));
+    const int sms = num_sms();
+    if (sms <= 0) return DSA_ERR_CUDA;
+    const int64_t blocks = (T + P.tokens - 1) / P.tokens;
+    const int grid = (int)std::min<int64_t>(blocks, 8ll * sms);
+    LaunchScope ls(K_ROPE, s);
+    if (dtype == DSA_BF16) {
+        if (inter) rope_kernel<__nv_bfloat16, true><<<grid, kRopeThreads, 0, s>>>(P);
+        else rope_kernel<__nv_bfloat16, false><<<grid, kRopeThreads, 0, s>>>(P);
+    } else {
+        if (inter) rope_kernel<float, true><<<grid, kRopeThreads, 0, s>>>(P);
+        else rope_kernel<float, false><<<grid, kRopeThreads, 0, s>>>(P);
+    }
+    return launch_status();
+}
+
+// ------------------------------------------------------------------ paged 8-bit cache
+bool page_supported(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+int log2_of(int x) { return 31 - __builtin_clz((unsigned)x); }
+
+template <int FMT>
+dsa_status launch_append_t(const AppendParams& P, int64_t units, cudaStream_t s) {
+    auto kern = kv_append_kernel<FMT>;
+    static DeviceFlags attr_set;
+    if (!set_smem_limit(kern, 128 * (kKvD / 2) * 8, attr_set)) return DSA_ERR_CUDA;
+    const int page = 1 << P.page_shift;
+    const int tokens = P.cu_new ? page : 1;  // most tokens of a block
+    const int threads = std::min(512, std::max(128, tokens * P.Hkv * kKvUnits / kAppendPasses));
+    LaunchScope ls(K_KV_APPEND, s);
+    kern<<<dim3((unsigned)units, 2), threads, tokens * P.n * 8, s>>>(P);
+    return launch_status();
+}
+
+size_t paged_ws_bytes(int Hq) { return align_up((size_t)2 * kPagedPartCtas * Hq * kPagedPartStride * 4, 256); }
+
+dsa_status run_paged_attn(const PagedParams& P, int fmt, cudaStream_t s) {
+    LaunchScope ls(K_PAGED_ATTN, s);
+    const dim3 grid(P.T, P.Hkv);
+    if (fmt == DSA_KV_E4M3) paged_attn_kernel<KV_E4M3><<<grid, 128, 0, s>>>(P);
+    else paged_attn_kernel<KV_INT8><<<grid, 128, 0, s>>>(P);
+    return launch_status();
+}
+
 // ------------------------------------------------------------------ decode helpers
 // Sequences whose ctx_len is out of range must not be read past the caches by the other kernels;
 // the indexer, top-k and attention kernels clamp their key counts to the cache capacity, and the
@@ -675,6 +740,7 @@ size_t dsa_workspace_size(int op, int64_t L, int B, int Hq, int HI, int topk) {
         return align_up(chunk_bytes(rows, ld, Hq), 256);
     }
     if (L <= 0 || topk <= 0 || HI <= 0) return 0;
+    if (op == DSA_OP_PAGED_ATTN) return B > 0 && Hq > 0 ? paged_ws_bytes(Hq) : 0;
     switch (op) {
     case DSA_OP_INDEX:
     case DSA_OP_TOPK:
@@ -908,6 +974,154 @@ dsa_status dsa_decode_noalloc(const void* q, const void* qI, const void* w, cons
 }
 
 size_t dsa_decode_noalloc_scratch_bytes(void) { return kNoAllocScratchBytes; }
+
+dsa_status dsa_rope(const void* x, int dtype, int64_t T, int H, int D, int64_t x_ts, int64_t x_hs, const int32_t* pos,
+                    int64_t pos0, const double* inv_freq, int rot_offset, int rot_dim, int layout, float mscale,
+                    int inverse, void* out, int64_t out_ts, int64_t out_hs, dsa_stream_t stream) {
+    if (!x || !out || !inv_freq || !aligned16(x) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(inv_freq) & 7u) || (reinterpret_cast<uintptr_t>(pos) & 3u))
+        return DSA_ERR_INVALID_ARG;
+    if (T <= 0 || H <= 0 || D <= 0 || rot_dim <= 0 || rot_offset < 0 || rot_offset + (int64_t)rot_dim > D)
+        return DSA_ERR_INVALID_ARG;
+    if (dtype != DSA_BF16 && dtype != DSA_FP32) return DSA_ERR_INVALID_ARG;
+    if (layout != DSA_ROPE_HALF && layout != DSA_ROPE_INTERLEAVED) return DSA_ERR_INVALID_ARG;
+    if (!(mscale == mscale) || x_ts < 0 || x_hs < 0 || out_ts < 0 || out_hs < 0) return DSA_ERR_INVALID_ARG;
+    if (!pos && (pos0 < -(int64_t(1) << 31) || pos0 > (int64_t(1) << 31) - T)) return DSA_ERR_INVALID_ARG;
+    if (D % 8 || D > 512 || rot_dim % 16 || rot_dim > 256 || rot_offset % 8 || H > 4096 || T > (int64_t)INT32_MAX)
+        return DSA_ERR_UNSUPPORTED;
+    const int V = dtype == DSA_BF16 ? 8 : 4, es = dtype == DSA_BF16 ? 2 : 4;
+    if (x_ts % V || x_hs % V || out_ts % V || out_hs % V) return DSA_ERR_INVALID_ARG;
+    const int64_t most = int64_t(1) << 40;  // keeps the extents below from wrapping
+    if (x_ts > most || x_hs > most || out_ts > most || out_hs > most) return DSA_ERR_INVALID_ARG;
+    if (!rows_disjoint(T, H, D, out_ts, out_hs)) return DSA_ERR_INVALID_ARG;
+    const bool in_place = x == out && (T == 1 || x_ts == out_ts) && (H == 1 || x_hs == out_hs);
+    if (!in_place) {
+        using u128 = unsigned __int128;
+        const u128 xa = reinterpret_cast<uintptr_t>(x), oa = reinterpret_cast<uintptr_t>(out);
+        const u128 xn = ((u128)(T - 1) * x_ts + (u128)(H - 1) * x_hs + D) * es;
+        const u128 on = ((u128)(T - 1) * out_ts + (u128)(H - 1) * out_hs + D) * es;
+        if (xa < oa + on && oa < xa + xn) return DSA_ERR_INVALID_ARG;
+    }
+    RopeParams P{};
+    P.out = out;
+    P.pos = pos;
+    P.pos0 = pos0;
+    P.inv_freq = inv_freq;
+    P.x_ts = x_ts, P.x_hs = x_hs, P.out_ts = out_ts, P.out_hs = out_hs;
+    P.n = rot_dim / 2, P.off = rot_offset;
+    P.mscale = mscale;
+    P.inverse = inverse != 0;
+    return run_rope(x, dtype, T, H, D, P, in_place, layout == DSA_ROPE_INTERLEAVED,
+                    reinterpret_cast<cudaStream_t>(stream));
+}
+
+dsa_status dsa_rope_freqs(int rot_dim, double theta, int scaling, double factor, double orig_len, double beta_fast,
+                          double beta_slow, double* inv_freq, float* mscale) {
+    if (!inv_freq || rot_dim <= 0 || rot_dim % 2 || !(theta > 1.0) || !std::isfinite(theta)) return DSA_ERR_INVALID_ARG;
+    if (scaling < DSA_ROPE_PLAIN || scaling > DSA_ROPE_YARN) return DSA_ERR_INVALID_ARG;
+    if (scaling != DSA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return DSA_ERR_INVALID_ARG;
+    if (scaling == DSA_ROPE_NTK && rot_dim <= 2) return DSA_ERR_INVALID_ARG;
+    if (scaling == DSA_ROPE_YARN && (!(orig_len > 0.0) || !(beta_slow > 0.0) || !(beta_fast > beta_slow)))
+        return DSA_ERR_INVALID_ARG;
+    const int n = rot_dim / 2;
+    double base = theta, lo = 0.0, hi = 1.0;
+    if (scaling == DSA_ROPE_NTK) base = theta * std::pow(factor, rot_dim / double(rot_dim - 2));
+    if (scaling == DSA_ROPE_YARN) {
+        // pair i turns orig_len * theta^(-i/n) / (2 pi) times over orig_len positions; the pairs that turn
+        // beta_fast and beta_slow times bound the ramp
+        const double two_pi = 6.283185307179586;
+        lo = n * std::log(orig_len / (beta_fast * two_pi)) / std::log(theta);
+        hi = n * std::log(orig_len / (beta_slow * two_pi)) / std::log(theta);
+        lo = std::max(0.0, std::floor(lo));
+        hi = std::min(double(n - 1), std::ceil(hi));
+        if (!(hi > lo)) hi = lo + 0.001;
+    }
+    for (int i = 0; i < n; ++i) {
+        double f = std::pow(base, -double(i) / n);
+        if (scaling == DSA_ROPE_LINEAR) f /= factor;
+        if (scaling == DSA_ROPE_YARN) {
+            const double r = std::min(1.0, std::max(0.0, (i - lo) / (hi - lo)));  // 0: kept, 1: divided
+            f = f * (1.0 - r) + f / factor * r;
+        }
+        inv_freq[i] = f;
+    }
+    if (mscale) *mscale = scaling == DSA_ROPE_YARN && factor > 1.0 ? (float)(0.1 * std::log(factor) + 1.0) : 1.f;
+    return DSA_OK;
+}
+
+dsa_status dsa_kv_append(const void* k_new, const void* v_new, int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs,
+                         int64_t N, const int32_t* cu_new, const int32_t* ctx_len, const int32_t* rope_pos,
+                         const double* inv_freq, int rot_offset, int rot_dim, int layout, float mscale, int kv_format,
+                         void* k_pages, void* v_pages, float* k_scale, float* v_scale, const int32_t* page_table,
+                         int B, int num_pages, int page_size, int max_pages, int Hkv, int D, dsa_stream_t stream) {
+    for (const void* p : {k_new, v_new, (const void*)k_pages, (const void*)v_pages})
+        if (!p || !aligned16(p)) return DSA_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)ctx_len, (const void*)k_scale, (const void*)v_scale, (const void*)page_table})
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return DSA_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)cu_new, (const void*)rope_pos})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return DSA_ERR_INVALID_ARG;
+    if (N <= 0 || B <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0 || Hkv <= 0 || D <= 0)
+        return DSA_ERR_INVALID_ARG;
+    if (!cu_new && N != B) return DSA_ERR_INVALID_ARG;
+    if (k_ts < 0 || k_hs < 0 || v_ts < 0 || v_hs < 0 || k_ts % 8 || k_hs % 8 || v_ts % 8 || v_hs % 8)
+        return DSA_ERR_INVALID_ARG;
+    if (kv_format != DSA_KV_E4M3 && kv_format != DSA_KV_INT8) return DSA_ERR_INVALID_ARG;
+    if (rot_dim < 0) return DSA_ERR_INVALID_ARG;
+    if (rot_dim) {
+        if (!inv_freq || (reinterpret_cast<uintptr_t>(inv_freq) & 7u)) return DSA_ERR_INVALID_ARG;
+        if (layout != DSA_ROPE_HALF && layout != DSA_ROPE_INTERLEAVED) return DSA_ERR_INVALID_ARG;
+        if (rot_offset < 0 || rot_offset + (int64_t)rot_dim > D || !(mscale == mscale)) return DSA_ERR_INVALID_ARG;
+        if (rot_dim % 16 || rot_offset % 8) return DSA_ERR_UNSUPPORTED;
+    }
+    if (D != kKvD || !(Hkv == 1 || Hkv == 2 || Hkv == 4) || !page_supported(page_size)) return DSA_ERR_UNSUPPORTED;
+    if (N >= (1 << 30) || B >= (1 << 29) || (int64_t)max_pages * page_size > (int64_t)INT32_MAX)
+        return DSA_ERR_UNSUPPORTED;
+    AppendParams P{};
+    P.k_new = static_cast<const __nv_bfloat16*>(k_new), P.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    P.k_ts = k_ts, P.k_hs = k_hs, P.v_ts = v_ts, P.v_hs = v_hs;
+    P.k_pages = static_cast<uint8_t*>(k_pages), P.v_pages = static_cast<uint8_t*>(v_pages);
+    P.k_scale = k_scale, P.v_scale = v_scale;
+    P.table = page_table, P.ctx_len = ctx_len, P.cu_new = cu_new, P.rope_pos = rope_pos, P.inv_freq = inv_freq;
+    P.B = B, P.N = (int)N, P.Hkv = Hkv, P.page_shift = log2_of(page_size), P.max_pages = max_pages;
+    P.num_pages = num_pages;
+    P.n = rot_dim / 2, P.off = rot_offset, P.inter = layout == DSA_ROPE_INTERLEAVED, P.mscale = mscale;
+    const int64_t units = cu_new ? (N >> P.page_shift) + 2 * (int64_t)B : B;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return kv_format == DSA_KV_E4M3 ? launch_append_t<KV_E4M3>(P, units, s) : launch_append_t<KV_INT8>(P, units, s);
+}
+
+dsa_status dsa_paged_attn(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                          const float* v_scale, const int32_t* page_table, const int32_t* seq, const int32_t* n_keys,
+                          const int32_t* idx, int kv_format, int T, int B, int num_pages, int page_size, int max_pages,
+                          int Hq, int Hkv, int D, int topk, float scale, void* out, float* lse, void* ws,
+                          size_t ws_bytes, dsa_stream_t stream) {
+    for (const void* p : {q, k_pages, v_pages, (const void*)out})
+        if (!p || !aligned16(p)) return DSA_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)k_scale, (const void*)v_scale, (const void*)page_table, (const void*)n_keys})
+        if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return DSA_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)seq, (const void*)idx, (const void*)lse})
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return DSA_ERR_INVALID_ARG;
+    if (T <= 0 || B <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0 || !(scale == scale))
+        return DSA_ERR_INVALID_ARG;
+    if ((!seq && T != B) || (idx && topk <= 0)) return DSA_ERR_INVALID_ARG;
+    if (kv_format != DSA_KV_E4M3 && kv_format != DSA_KV_INT8) return DSA_ERR_INVALID_ARG;
+    dsa_status st = check_attn_shape(Hq, Hkv, D);
+    if (st != DSA_OK) return st;
+    if (!page_supported(page_size) || (idx && topk > kMaxTopk) || (int64_t)max_pages * page_size > (int64_t)INT32_MAX)
+        return DSA_ERR_UNSUPPORTED;
+    if (!ws || !aligned16(ws) || ws_bytes < paged_ws_bytes(Hq)) return DSA_ERR_WORKSPACE;
+    PagedParams P{};
+    P.q = static_cast<const __nv_bfloat16*>(q);
+    P.k_pages = static_cast<const uint8_t*>(k_pages), P.v_pages = static_cast<const uint8_t*>(v_pages);
+    P.k_scale = k_scale, P.v_scale = v_scale, P.table = page_table, P.seq = seq, P.n_keys = n_keys, P.idx = idx;
+    P.T = T, P.B = B, P.num_pages = num_pages, P.page_shift = log2_of(page_size), P.max_pages = max_pages;
+    P.Hq = Hq, P.Hkv = Hkv, P.topk = idx ? topk : 0;
+    P.scale_log2 = scale * 1.4426950408889634f;
+    P.out = static_cast<__nv_bfloat16*>(out);
+    P.lse = lse;
+    P.part = static_cast<float*>(ws);
+    return run_paged_attn(P, kv_format, reinterpret_cast<cudaStream_t>(stream));
+}
 
 dsa_status dsa_sync_status(dsa_stream_t stream) {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return DSA_ERR_CUDA;

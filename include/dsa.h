@@ -53,7 +53,14 @@ typedef enum {
 
 /* Workspace kinds for dsa_workspace_size(). */
 enum { DSA_OP_INDEX = 0, DSA_OP_TOPK = 1, DSA_OP_SPARSE_ATTN = 2, DSA_OP_PREFILL = 3, DSA_OP_DECODE = 4,
-       DSA_OP_INDEXER_KL = 5 };
+       DSA_OP_INDEXER_KL = 5, DSA_OP_PAGED_ATTN = 6 };
+
+/* Element types of dsa_rope; pairings of rotated dims; formats of the paged 8-bit KV cache. */
+enum { DSA_BF16 = 0, DSA_FP32 = 1 };
+enum { DSA_ROPE_HALF = 0, DSA_ROPE_INTERLEAVED = 1 };
+enum { DSA_KV_E4M3 = 0, DSA_KV_INT8 = 1 };
+/* Scalings of dsa_rope_freqs. */
+enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_NTK = 2, DSA_ROPE_YARN = 3 };
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *dsa_status_string(int status);
@@ -239,11 +246,115 @@ dsa_status dsa_decode_noalloc(const void *q, const void *qI, const void *w, cons
 size_t dsa_decode_noalloc_scratch_bytes(void);
 
 /*
+ * Rotary positions: every head of x has rot_dim = 2n of its D dims turned, in pairs, by the token's
+ * position.  For token t at position p (pos[t], or pos0 + t where pos is NULL) and pair i < n:
+ *   a = p * inv_freq[i]
+ *   out[t,h,A_i] = mscale * (x[t,h,A_i] cos a - x[t,h,B_i] sin a)
+ *   out[t,h,B_i] = mscale * (x[t,h,A_i] sin a + x[t,h,B_i] cos a)
+ *   (A_i, B_i) = (rot_offset + i, rot_offset + n + i)        layout DSA_ROPE_HALF
+ *              = (rot_offset + 2i, rot_offset + 2i + 1)      layout DSA_ROPE_INTERLEAVED
+ * The other dims are copied as they are.  inverse != 0 turns by -a (the same mscale): that is the
+ * gradient with respect to x, given the gradient with respect to out as x.
+ *   x, out    [T, H, D] of dtype DSA_BF16 or DSA_FP32 with x_ts/out_ts elements between tokens and
+ *             x_hs/out_hs between heads (dims are adjacent); strides are multiples of 16 bytes, x's
+ *             may be 0.  out's rows must not overlap one another.  out may be x itself (same pointer
+ *             and strides); otherwise their address ranges must not overlap.
+ *   pos       int32 [T] (any value, in any order) or NULL; pos0 + T <= 2^31
+ *   inv_freq  double [rot_dim / 2] on the device, radians per position, finite (dsa_rope_freqs
+ *             computes the usual ones).  The angle is exact to 2^-53 of a turn per position.
+ * Sums and products are fp32, rounded once.  Supported: D a multiple of 8 up to 512, rot_dim a
+ * multiple of 16 from 16 to min(D, 256), rot_offset a multiple of 8 with rot_offset + rot_dim <= D,
+ * H <= 4096, T < 2^31.
+ */
+dsa_status dsa_rope(const void *x, int dtype, int64_t T, int H, int D, int64_t x_ts, int64_t x_hs, const int32_t *pos,
+                    int64_t pos0, const double *inv_freq, int rot_offset, int rot_dim, int layout, float mscale,
+                    int inverse, void *out, int64_t out_ts, int64_t out_hs, dsa_stream_t stream);
+
+/*
+ * Frequencies for dsa_rope and dsa_kv_append, computed on the HOST into inv_freq (host memory,
+ * rot_dim / 2 doubles), and the factor that belongs to them into *mscale (host, may be NULL).
+ *   DSA_ROPE_PLAIN   theta^(-2i / rot_dim); mscale 1 (factor and the rest are ignored)
+ *   DSA_ROPE_LINEAR  the same / factor: positions interpolated; mscale 1
+ *   DSA_ROPE_NTK     the same with theta * factor^(rot_dim / (rot_dim - 2)) for theta: the slowest
+ *                    frequency is divided by factor, the fastest kept; mscale 1
+ *   DSA_ROPE_YARN    pairs that turn more than beta_fast times over orig_len positions are kept,
+ *                    those that turn less than beta_slow times are divided by factor, with a linear
+ *                    ramp over the pair index between; mscale = 0.1 ln(factor) + 1 (factor > 1)
+ * Errors: DSA_ERR_INVALID_ARG unless rot_dim is a positive even number, theta > 1, factor >= 1 (all but
+ * PLAIN) and, for YARN, orig_len > 0 and beta_fast > beta_slow > 0; NTK needs rot_dim > 2.
+ */
+dsa_status dsa_rope_freqs(int rot_dim, double theta, int scaling, double factor, double orig_len, double beta_fast,
+                          double beta_slow, double *inv_freq, float *mscale);
+
+/*
+ * Append keys and values to a paged 8-bit cache, with the position rotation of the keys on the way.
+ *   k_new, v_new  bf16 [N, Hkv, D] with *_ts elements between tokens and *_hs between heads
+ *                 (multiples of 8; slices of a fused projection are fine)
+ *   cu_new        int32 [B + 1], ascending: tokens cu_new[b] .. cu_new[b+1]-1 belong to sequence b
+ *                 (none is allowed); tokens outside all of them are ignored.  NULL: N == B, one
+ *                 token each.
+ *   ctx_len       int32 [B]: tokens already cached.  Token i of sequence b goes to position
+ *                 ctx_len[b] + i.  ctx_len is not changed.
+ *   page_table    int32 [B, max_pages]: position p lies in page page_table[b, p / page_size], slot
+ *                 p mod page_size.  Only entries of touched pages are read.  A page belongs to
+ *                 one sequence.
+ *   k_pages, v_pages  [num_pages, page_size, Hkv, D] bytes, format DSA_KV_E4M3 or DSA_KV_INT8
+ *   k_scale, v_scale  fp32 [num_pages, Hkv]: a byte stands for scale * its e4m3 or int8 value
+ *   rot_dim       0: keys are stored as they come.  Otherwise keys are turned as by dsa_rope
+ *                 (inv_freq, rot_offset, layout, mscale) at position rope_pos[n], int32 [N], or
+ *                 where rope_pos is NULL at the cache position; the turned value is not rounded in
+ *                 between.
+ * A scale is the least power of two (2^-64 at least) with which the page's largest magnitude of
+ * that head fits 448 (e4m3) or 127 (int8).  Writing slot 0 starts a page anew, whatever it held;
+ * otherwise the page's scale never falls, and when it rises the tokens in the slots before the new
+ * ones are rounded again to the new scale.  Slots behind the new tokens are not touched.
+ * Rounding is to nearest, ties to even.  Infinities count neither for the scale nor exceed it: they
+ * become the largest value; NaN stays NaN in e4m3 and becomes 0 in int8 (all this of the turned keys),
+ * reported by dsa_sync_status() as DSA_ERR_DEVICE_INPUT, as are a ctx_len or cu_new out of range
+ * (that sequence is skipped) and a page number outside [0, num_pages) (that page is skipped).
+ * Supported: D = 128, Hkv in {1, 2, 4}, page_size in {16, 32, 64, 128}, rot_dim a multiple of 16 up to
+ * 128, N < 2^30, B < 2^29, max_pages * page_size < 2^31.
+ */
+dsa_status dsa_kv_append(const void *k_new, const void *v_new, int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs,
+                         int64_t N, const int32_t *cu_new, const int32_t *ctx_len, const int32_t *rope_pos,
+                         const double *inv_freq, int rot_offset, int rot_dim, int layout, float mscale, int kv_format,
+                         void *k_pages, void *v_pages, float *k_scale, float *v_scale, const int32_t *page_table,
+                         int B, int num_pages, int page_size, int max_pages, int Hkv, int D, dsa_stream_t stream);
+
+/*
+ * Attention over the paged 8-bit cache that dsa_kv_append fills.  Row t of q is one query token:
+ *   q           bf16 [T, Hq, D], positions already rotated
+ *   seq         int32 [T]: the row's sequence, or NULL (T == B, row t is sequence t's).  Several
+ *               rows may share a sequence (speculated tokens, a chunk of a prefill).
+ *   n_keys      int32 [T]: the row attends to positions 0 .. n_keys[t]-1 of its sequence (for a
+ *               decode step ctx_len + 1 after the append; causal rows differ by one).  0 is allowed.
+ *   idx         int32 [T, topk] or NULL.  With idx (as dsa_topk writes it) only the keys named by the
+ *               first min(topk, n_keys[t]) entries are read; entries < 0 or >= n_keys[t] are
+ *               skipped, one that is repeated counts as often as it stands there.
+ *   out         bf16 [T, Hq, D];  lse  fp32 [T, Hq] natural-log sum-exp, or NULL
+ * A row without keys gets out = 0 and lse = -inf.  The cache, its scales and page_table as for
+ * dsa_kv_append; any finite scales will do (those of dsa_kv_append are powers of two).  Only pages
+ * that hold attended keys are read, and of those only attended tokens.
+ *   ws          device workspace of at least dsa_workspace_size(DSA_OP_PAGED_ATTN, L, T, Hq, HI, topk)
+ *               bytes (which depends on Hq alone); one call at a time may use it
+ * A row whose seq or n_keys is out of range counts as empty and a key whose page number is outside
+ * [0, num_pages) is skipped; dsa_sync_status() reports both as DSA_ERR_DEVICE_INPUT.
+ * Supported: D = 128, Hkv in {1, 2, 4}, Hq / Hkv <= 16, page_size in {16, 32, 64, 128}, topk <= 65536,
+ * max_pages * page_size < 2^31.
+ */
+dsa_status dsa_paged_attn(const void *q, const void *k_pages, const void *v_pages, const float *k_scale,
+                          const float *v_scale, const int32_t *page_table, const int32_t *seq, const int32_t *n_keys,
+                          const int32_t *idx, int kv_format, int T, int B, int num_pages, int page_size, int max_pages,
+                          int Hq, int Hkv, int D, int topk, float scale, void *out, float *lse, void *ws,
+                          size_t ws_bytes, dsa_stream_t stream);
+
+/*
  * Bytes of workspace an entry point needs.  op: DSA_OP_*.  L: sequence length (prefill) or cache
  * capacity Lmax (decode); B: sequences (decode); Hq: query heads; HI: indexer heads; topk.
  * DSA_OP_PREFILL returns the recommended size (score rows of up to 16 GiB per chunk plus index
  * rows; a smaller workspace works too, in more and shorter chunks, somewhat slower);
  * DSA_OP_INDEXER_KL the score rows alone, up to 4 GiB per chunk (topk ignored);
+ * DSA_OP_PAGED_ATTN depends on Hq alone (L, B, HI and topk must be positive all the same);
  * DSA_OP_INDEX/TOPK/SPARSE_ATTN return 0.  Returns 0 for invalid arguments.
  */
 size_t dsa_workspace_size(int op, int64_t L, int B, int Hq, int HI, int topk);
@@ -267,9 +378,10 @@ unsigned int dsa_error_site(void);
  * events, stops recording and returns, per kernel kind, the number of launches and the total
  * milliseconds.  Kinds: 0 indexer, 1 top-k, 2 sparse attention, 3 split combine, 4 decode
  * append and 5 context advance (both now done inside other kernels: always 0), 6 self-test,
- * 7 indexer warm-up KL.  Arrays have DSA_PROFILE_KINDS entries.
+ * 7 indexer warm-up KL, 8 rotary positions, 9 paged-cache append, 10 paged-cache attention (its
+ * merge of splits counts under 3).  Arrays have DSA_PROFILE_KINDS entries.
  */
-#define DSA_PROFILE_KINDS 8
+#define DSA_PROFILE_KINDS 11
 void dsa_profile_begin(void);
 dsa_status dsa_profile_end(int64_t *launches, double *total_ms);
 

@@ -519,14 +519,55 @@ dsa_status launch_append_t(const AppendParams& P, int64_t units, cudaStream_t s)
     return launch_status();
 }
 
-size_t paged_ws_bytes(int Hq) { return align_up((size_t)2 * kPagedPartCtas * Hq * kPagedPartStride * 4, 256); }
+// Workspace: two partials for each block that shares rows, then the rows' first tiles.
+size_t paged_part_bytes(int Hq) { return align_up((size_t)2 * kPagedPartCtas * Hq * kPagedPartStride * 4, 256); }
+size_t paged_ws_bytes(int Hq) { return paged_part_bytes(Hq) + align_up((size_t)(kPagedSharedRows + 1) * 8, 256); }
 
-dsa_status run_paged_attn(const PagedParams& P, int fmt, cudaStream_t s) {
-    LaunchScope ls(K_PAGED_ATTN, s);
-    const dim3 grid(P.T, P.Hkv);
-    if (fmt == DSA_KV_E4M3) paged_attn_kernel<KV_E4M3><<<grid, 128, 0, s>>>(P);
-    else paged_attn_kernel<KV_INT8><<<grid, 128, 0, s>>>(P);
-    return launch_status();
+template <int WPH>
+cudaError_t launch_combine_t(const PagedParams& P, int TK, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(P.T, std::max(1, std::min((P.Hq + 8 / WPH - 1) / (8 / WPH), 1184 / P.T)));
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];  // may start before the attention kernel ends; it waits for that itself
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<WPH>, P, TK);
+}
+
+template <int FMT, int NT>
+dsa_status launch_paged_t(PagedParams P, cudaStream_t s) {
+    using C = PagedCfg<NT>;
+    auto kern = paged_attn_kernel<FMT, NT>;
+    static DeviceFlags attr_set;
+    if (!set_smem_limit(kern, C::SMEM, attr_set)) return DSA_ERR_CUDA;
+    const int sms = num_sms();
+    if (sms <= 0) return DSA_ERR_CUDA;
+    P.shared_rows = P.T <= kPagedSharedRows;
+    const int grid = P.shared_rows ? std::min(C::CTAS * sms, kPagedPartCtas) : P.T;
+    {
+        LaunchScope ls(K_PAGED_ATTN, s);
+        kern<<<grid, C::THREADS, C::SMEM, s>>>(P);
+        const dsa_status st = launch_status();
+        if (st != DSA_OK || !P.shared_rows) return st;
+    }
+    // 8 warps on a head while there are few (row, head) pairs, down to one
+    LaunchScope ls(K_COMBINE, s);
+    const int TK = 16 * C::NW / P.Hkv, pairs = P.T * P.Hq;
+    const cudaError_t e = pairs <= 1184 ? launch_combine_t<8>(P, TK, s)
+                          : pairs <= 2368 ? launch_combine_t<4>(P, TK, s)
+                          : pairs <= 4736 ? launch_combine_t<2>(P, TK, s) : launch_combine_t<1>(P, TK, s);
+    return e == cudaSuccess ? launch_status() : DSA_ERR_CUDA;
+}
+
+dsa_status run_paged_attn(PagedParams P, int fmt, void* ws, cudaStream_t s) {
+    P.part = static_cast<float*>(ws);
+    P.row_start = reinterpret_cast<long long*>(static_cast<uint8_t*>(ws) + paged_part_bytes(P.Hq));
+    const bool two = P.Hq / P.Hkv > 8;
+    if (fmt == DSA_KV_E4M3) return two ? launch_paged_t<KV_E4M3, 2>(P, s) : launch_paged_t<KV_E4M3, 1>(P, s);
+    return two ? launch_paged_t<KV_INT8, 2>(P, s) : launch_paged_t<KV_INT8, 1>(P, s);
 }
 
 // ------------------------------------------------------------------ decode helpers
@@ -1074,7 +1115,7 @@ dsa_status dsa_kv_append(const void* k_new, const void* v_new, int64_t k_ts, int
         if (rot_dim % 16 || rot_offset % 8) return DSA_ERR_UNSUPPORTED;
     }
     if (D != kKvD || !(Hkv == 1 || Hkv == 2 || Hkv == 4) || !page_supported(page_size)) return DSA_ERR_UNSUPPORTED;
-    if (N >= (1 << 30) || B >= (1 << 29) || (int64_t)max_pages * page_size > (int64_t)INT32_MAX)
+    if (N >= (1 << 30) || B >= (1 << 29) || (int64_t)max_pages * page_size > (1 << 30))
         return DSA_ERR_UNSUPPORTED;
     AppendParams P{};
     P.k_new = static_cast<const __nv_bfloat16*>(k_new), P.v_new = static_cast<const __nv_bfloat16*>(v_new);
@@ -1107,7 +1148,8 @@ dsa_status dsa_paged_attn(const void* q, const void* k_pages, const void* v_page
     if (kv_format != DSA_KV_E4M3 && kv_format != DSA_KV_INT8) return DSA_ERR_INVALID_ARG;
     dsa_status st = check_attn_shape(Hq, Hkv, D);
     if (st != DSA_OK) return st;
-    if (!page_supported(page_size) || (idx && topk > kMaxTopk) || (int64_t)max_pages * page_size > (int64_t)INT32_MAX)
+    if (!page_supported(page_size) || (idx && topk > kMaxTopk)) return DSA_ERR_UNSUPPORTED;
+    if ((int64_t)max_pages * page_size > (1 << 30) || (int64_t)num_pages * page_size > (int64_t)INT32_MAX)
         return DSA_ERR_UNSUPPORTED;
     if (!ws || !aligned16(ws) || ws_bytes < paged_ws_bytes(Hq)) return DSA_ERR_WORKSPACE;
     PagedParams P{};
@@ -1119,8 +1161,7 @@ dsa_status dsa_paged_attn(const void* q, const void* k_pages, const void* v_page
     P.scale_log2 = scale * 1.4426950408889634f;
     P.out = static_cast<__nv_bfloat16*>(out);
     P.lse = lse;
-    P.part = static_cast<float*>(ws);
-    return run_paged_attn(P, kv_format, reinterpret_cast<cudaStream_t>(stream));
+    return run_paged_attn(P, kv_format, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 dsa_status dsa_sync_status(dsa_stream_t stream) {

@@ -1,15 +1,35 @@
 // Attention over the paged 8-bit KV cache (kv8.cuh): row t reads keys of sequence seq[t],
-//   z_s = scale * 2^ek(s) * sum_d q[t,h,d] k8[s,d],  out = sum_s softmax(z)_s 2^ev(s) v8[s,:]
-// over all its n_keys[t] cached keys, or over those that idx names.
+//   z_s = scale * ks(s) * sum_d q[t,h,d] k8[s,d],  out = sum_s softmax(z)_s vs(s) v8[s,:]
+// over all its n_keys[t] cached keys, or over those that idx names; ks, vs are the scales of the key's page.
+//
+// Bound by the cache's bytes: at 32 query and 4 KV heads a key is 1 KB against 16 Kflop.
+//   - A warp works alone: it owns one KV head and 16 keys of every tile, copies their K and V rows
+//     (16 x 128 bytes each) and scales into a ring of its own with cp.async and multiplies them, so
+//     that no barrier stands between copies and products and every SM keeps 16 rings in flight.
+//     Dense rows and selected keys differ only in where a lane's key number comes from.
+//   - Both products run on fp16 matrix instructions, where e4m3 and int8 values are exact:
+//     S^T[keys x heads] = K Q^T and O^T += V^T P^T, the G query heads of the KV head as columns.  The rows
+//     of the fragments stand for whichever keys and dims make a thread's bytes adjacent, so K and V go
+//     from shared memory to fragments by 16-byte loads; K's 16-byte chunks are exchanged by key parity
+//     and V's by key pair, which keeps those loads free of bank conflicts.
+//   - q goes to fp16 after its head is scaled by a power of two to at most 2^14: no bit of bf16's is lost
+//     within 2^-28 of the head's largest.
+//   - V's scale 2^e * m, 1 <= m < 2, enters through the exponent: the softmax's reference is the running
+//     maximum of z + e, so that P = 2^(z + e - max) * m, rounded to fp16, keeps its bits however far the
+//     scales of a row's pages lie apart; the row sum adds P's 2^-e part in fp32.
+//   - Rows are dealt to blocks by tiles: block c of C takes tiles [c, c + 1) * ceil(W / C) of all rows' W, in
+//     order, whatever the rows' lengths.  A row that one block holds whole is finished there; of the
+//     others each block writes its unnormalised part, and paged_combine_kernel joins them.
 #pragma once
 
 #include "kv8.cuh"
 
 namespace dsa {
 
-constexpr int kPagedMaxG = 16;
-constexpr int kPagedPartCtas = 296;  // split partials in the workspace: two for each of so many CTAs
-constexpr int kPagedPartStride = kKvD + 4;
+constexpr int kPagedPartCtas = 296;     // most blocks that share rows; each has two partial slots
+constexpr int kPagedSharedRows = 1184;  // with more rows, every row gets a block of its own
+constexpr int kPagedPartStride = kKvD + 4;  // floats of a partial: O[128], max, sum, 2 pad
+constexpr int kPagedMinTiles = 2;       // fewest tiles worth a block of their own
 
 struct PagedParams {
     const __nv_bfloat16* q;            // [T, Hq, 128]
@@ -23,7 +43,24 @@ struct PagedParams {
     float scale_log2;
     __nv_bfloat16* out;                // [T, Hq, 128]
     float* lse;                        // [T, Hq], may be null
-    float* part;
+    int shared_rows;                   // rows are dealt by tiles (and joined); otherwise one block each
+    float* part;                       // [2 * gridDim.x, Hq, kPagedPartStride]
+    long long* row_start;              // [T + 1]: the rows' first tiles, and the tiles of a block behind them
+};
+
+// NT: groups of 8 query heads of a KV head.  One group leaves registers for two blocks of 8 warps on an
+// SM; two groups take one block of 12.
+template <int NT>
+struct PagedCfg {
+    static constexpr int NW = NT == 1 ? 8 : 12;
+    static constexpr int S = NT == 1 ? 3 : 4;  // ring stages of a warp
+    static constexpr int THREADS = NW * 32;
+    static constexpr int CTAS = NT == 1 ? 2 : 1;
+    static constexpr int STAGE = 2 * 16 * kKvD;  // K rows, V rows
+    static constexpr int RING = NW * S * STAGE;
+    static constexpr int META = NW * S * (32 + 4) * 4;  // scales of 16 keys (K, V), mask, pad
+    static constexpr int XCH = (NW / 2) * (16 + 4 * NT) * 32 * 4;
+    static constexpr int SMEM = RING + META + XCH;
 };
 
 // Sequence and key count of row t; a bad one is reported and leaves the row empty.
@@ -36,74 +73,510 @@ __device__ __forceinline__ void paged_row(const PagedParams& P, int t, int& b, i
         b = 0, n = 0;
     }
 }
+__device__ __forceinline__ int paged_count(const PagedParams& P, int n) { return P.idx ? min(P.topk, n) : n; }
 
-// One block per (row, KV head); each warp takes every fourth key, a lane 4 dims of it.
-template <int FMT>
-__global__ void __launch_bounds__(128) paged_attn_kernel(const PagedParams P) {
-    __shared__ float sm[4][kPagedMaxG], sl[4][kPagedMaxG], so[4][kPagedMaxG][kKvD];
-    const int t = blockIdx.x, g = blockIdx.y, G = P.Hq / P.Hkv;
+__device__ __forceinline__ void cp_async_4(void* dst, const void* src, bool valid) {
+    const int n = valid ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two stored bytes (of the low or the high half of w) as fp16 values.
+template <int FMT, bool HI>
+__device__ __forceinline__ uint32_t kv_f16x2(uint32_t w) {
+    if constexpr (FMT == KV_E4M3) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(HI ? w >> 16 : w)));
+        return r;
+    } else {
+        // byte + 128 in the low bits of the fp16 number 1024 is 1152 + byte
+        const uint32_t m = __byte_perm(w ^ 0x80808080u, 0x64646464u, HI ? 0x4342 : 0x4140);
+        const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&m), __half2half2(__ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    }
+}
+
+template <int FMT, int NT>
+__global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) paged_attn_kernel(const PagedParams P) {
+    using C = PagedCfg<NT>;
+    constexpr int NW = C::NW, S = C::S;
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int Hkv = P.Hkv, G = P.Hq / Hkv;
+    const int head = warp % Hkv, sub = warp / Hkv, nsub = NW / Hkv;
+    const int TK = 16 * nsub;  // keys of a tile
+    const int g = lane >> 2, j = lane & 3;
+
+    // ---- this block's tiles [w0, w1), from tile `tile0` of row `row0` on
+    long long w0 = 0, w1;
+    int row0 = blockIdx.x, tile0 = 0;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (P.shared_rows) {
+        __shared__ long long s_sum[NW], s_total;
+        __shared__ int s_row0, s_tile0;
+        const int per = (P.T + C::THREADS - 1) / C::THREADS;
+        const int r0 = min(P.T, (int)threadIdx.x * per), r1 = min(P.T, r0 + per);
+        long long mine = 0;
+        for (int r = r0; r < r1; ++r) {
+            int b, n;
+            paged_row(P, r, b, n);
+            mine += (paged_count(P, n) + TK - 1) / TK;
+        }
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        if (lane == 31) s_sum[warp] = incl;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            long long run = 0;
+            for (int w = 0; w < NW; ++w) {
+                const long long x = s_sum[w];
+                s_sum[w] = run;
+                run += x;
+            }
+            s_total = run;
+        }
+        __syncthreads();
+        const long long total = s_total;
+        const long long chunk = max((long long)kPagedMinTiles, (total + gridDim.x - 1) / gridDim.x);
+        w0 = blockIdx.x * chunk;
+        w1 = min(total, w0 + chunk);
+        long long start = s_sum[warp] + incl - mine;
+        if (blockIdx.x == 0 || (w0 >= start && w0 < start + mine)) {
+            for (int r = r0; r < r1; ++r) {
+                int b, n;
+                paged_row(P, r, b, n);
+                const int nt = (paged_count(P, n) + TK - 1) / TK;
+                if (w0 >= start && w0 < start + nt) s_row0 = r, s_tile0 = (int)(w0 - start);
+                if (blockIdx.x == 0) P.row_start[r] = start;
+                start += nt;
+            }
+        }
+        if (blockIdx.x == 0 && threadIdx.x == 0) P.row_start[P.T] = chunk;
+        __syncthreads();
+        if (w0 >= w1) return;
+        row0 = s_row0, tile0 = s_tile0;
+    } else {
+        int b, n;
+        paged_row(P, row0, b, n);
+        w1 = (paged_count(P, n) + TK - 1) / TK;
+        if (w1 == 0) {  // a row without keys
+            uint4* o = reinterpret_cast<uint4*>(P.out + (long long)row0 * P.Hq * kKvD);
+            for (int i = threadIdx.x; i < P.Hq * kKvD / 8; i += C::THREADS) o[i] = make_uint4(0, 0, 0, 0);
+            if (P.lse)
+                for (int h = threadIdx.x; h < P.Hq; h += C::THREADS) P.lse[(long long)row0 * P.Hq + h] = -INFINITY;
+            return;
+        }
+    }
+    const int tiles = (int)(w1 - w0);
+
+    uint8_t* ring = smem + warp * (S * C::STAGE);
+    float* meta = reinterpret_cast<float*>(smem + C::RING) + warp * (S * 36);
+    float* xch = reinterpret_cast<float*>(smem + C::RING + C::META);
+
+    // ---- copies.  A tile passes three steps, one iteration apart: its keys' numbers are loaded (lane
+    // i < 16: key i of this warp), their pages looked up, their rows copied.
+    int f_row = row0, f_tile = tile0, f_nt = 0, f_b = 0, f_n = 0, f_left = tiles;  // front cursor
+    if (tiles > 0) {
+        paged_row(P, f_row, f_b, f_n);
+        f_nt = (paged_count(P, f_n) + TK - 1) / TK;
+    }
+    int a_key = -1, a_n = 0, a_b = 0;  // key numbers loaded
+    int b_off = 0, b_pid = -1;         // pages looked up: -1 none
+    auto load_keys = [&]() {
+        a_key = -1;
+        if (f_left <= 0) return;
+        --f_left;
+        const int e = f_tile * TK + sub * 16 + lane;
+        a_n = f_n, a_b = f_b;
+        if (lane < 16 && e < paged_count(P, f_n)) a_key = P.idx ? P.idx[(long long)f_row * P.topk + e] : e;
+        if (++f_tile == f_nt && f_left > 0) {
+            do {
+                paged_row(P, ++f_row, f_b, f_n);
+                f_nt = (paged_count(P, f_n) + TK - 1) / TK;
+            } while (f_nt == 0);
+            f_tile = 0;
+        }
+    };
+    auto look_up = [&]() {
+        b_pid = -1;
+        if (a_key >= 0 && a_key < a_n) {
+            b_pid = P.table[(long long)a_b * P.max_pages + (a_key >> P.page_shift)];
+            b_off = a_key & ((1 << P.page_shift) - 1);
+            if (b_pid < 0 || b_pid >= P.num_pages) {
+                record_error(DSA_DEV_ERR_BOUNDS, 0xb02);
+                b_pid = -1;
+            }
+        }
+    };
+    auto copy_rows = [&](int st) {
+        const unsigned mask = __ballot_sync(0xffffffffu, b_pid >= 0);
+        float* sc = meta + st * 36;
+        if (lane == 0) reinterpret_cast<unsigned*>(sc)[32] = mask;
+        if (mask) {
+            uint8_t* dst = ring + st * C::STAGE;
+            const int slot = (b_pid << P.page_shift) + b_off;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = i * 4 + (lane >> 3), c = lane & 7;
+                const int s = __shfl_sync(0xffffffffu, slot, r);
+                const bool ok = mask >> r & 1;
+                const long long at = ok ? ((long long)s * Hkv + head) * kKvD + c * 16 : 0;
+                cp_async_16(dst + r * kKvD + ((c ^ ((r & 1) << 2)) << 4), P.k_pages + at, ok);
+                cp_async_16(dst + 16 * kKvD + r * kKvD + ((c ^ (r & 6)) << 4), P.v_pages + at, ok);
+            }
+            const int pid = __shfl_sync(0xffffffffu, b_pid, lane & 15);
+            const bool ok = mask >> (lane & 15) & 1;
+            cp_async_4(sc + lane, (lane < 16 ? P.k_scale : P.v_scale) + (ok ? (long long)pid * Hkv + head : 0), ok);
+        }
+        cp_async_commit();
+    };
+    load_keys();
+    look_up();
+    load_keys();
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) {
+        copy_rows(s);
+        look_up();
+        load_keys();
+    }
+
+    // ---- per row: queries, running maximum, sums, outputs
+    uint32_t qf[NT][8][2];
+    float qfac[NT][2];  // of heads nt * 8 + 2 j + {0, 1}: logits in log2 per unit of the product
+    float o[NT][8][4], m_run[NT][2], l_run[NT][2];
+    int row = row0, left;  // left: tiles of the row still to come in this block
+    bool whole;            // the block holds the row from its first tile to its last
+    long long at = w0;     // flat number of the next tile
+    bool first_part = true;
+    auto begin_row = [&](int tile) {
+        int b, n;
+        paged_row(P, row, b, n);
+        const int nt = (paged_count(P, n) + TK - 1) / TK;
+        left = (int)min((long long)(nt - tile), w1 - at);
+        whole = tile == 0 && left == nt;
+#pragma unroll
+        for (int nt8 = 0; nt8 < NT; ++nt8) {
+            const int hl = nt8 * 8 + g;
+            const __nv_bfloat16* qrow = P.q + ((long long)row * P.Hq + head * G + (hl < G ? hl : 0)) * kKvD;
+            float f[8][4], top = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                const uint2 w = *reinterpret_cast<const uint2*>(qrow + (kk < 4 ? j * 16 + kk * 4 : 64 + j * 16 + (kk - 4) * 4));
+                f[kk][0] = __uint_as_float(w.x << 16), f[kk][1] = __uint_as_float(w.x & 0xffff0000u);
+                f[kk][2] = __uint_as_float(w.y << 16), f[kk][3] = __uint_as_float(w.y & 0xffff0000u);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(f[kk][i]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // 2^s brings the head's largest below 2^14
+            int s = 13 - ((int)(__float_as_uint(top) >> 23) - 127);
+            s = max(-114, min(100, s));
+            const float up = hl < G ? kv_pow2(s) : 0.f;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+                qf[nt8][kk][0] = pack_f16x2(f[kk][0] * up, f[kk][1] * up);
+                qf[nt8][kk][1] = pack_f16x2(f[kk][2] * up, f[kk][3] * up);
+            }
+            const float fac = P.scale_log2 * kv_pow2(-s);
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+                qfac[nt8][jj] = __shfl_sync(0xffffffffu, fac, (2 * j + jj) * 4);
+                m_run[nt8][jj] = -INFINITY, l_run[nt8][jj] = 0.f;
+            }
+#pragma unroll
+            for (int dt = 0; dt < 8; ++dt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nt8][dt][i] = 0.f;
+        }
+    };
+    begin_row(tile0);
+
+    for (int i = 0, st = 0; i < tiles; ++i) {
+        cp_async_wait<S - 2>();
+        __syncwarp();
+        copy_rows(st == 0 ? S - 1 : st - 1);  // the stage that the last iteration used up
+        look_up();
+        load_keys();
+        const float* sc = meta + st * 36;
+        const unsigned mask = reinterpret_cast<const unsigned*>(sc)[32];
+        if (mask) {
+            const uint8_t* sk = ring + st * C::STAGE;
+            const uint8_t* sv = sk + 16 * kKvD;
+            // S^T: rows are keys g and g + 8; the dims of step kk are word kk of the thread's two chunks
+            float sacc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) sacc[nt][x] = 0.f;
+            {
+                const uint8_t* k0 = sk + g * kKvD + ((j ^ ((g & 1) << 2)) << 4);
+                const uint8_t* k1 = sk + g * kKvD + ((j ^ ((g & 1) << 2) ^ 4) << 4);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint8_t* p = half ? k1 : k0;
+                    const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 8 * kKvD);
+                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t a[4] = {kv_f16x2<FMT, false>(xw[w]), kv_f16x2<FMT, false>(yw[w]),
+                                               kv_f16x2<FMT, true>(xw[w]), kv_f16x2<FMT, true>(yw[w])};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_16816_f16(sacc[nt], a, qf[nt][half * 4 + w][0], qf[nt][half * 4 + w][1]);
+                    }
+                }
+            }
+            const bool v0 = mask >> g & 1, v1 = mask >> (g + 8) & 1;
+            const float ks0 = sc[g], ks1 = sc[g + 8], vs0 = sc[16 + g], vs1 = sc[24 + g];
+            const int e0 = min(120, max(-80, (int)(__float_as_uint(vs0) >> 23 & 255u) - 127));
+            const int e1 = min(120, max(-80, (int)(__float_as_uint(vs1) >> 23 & 255u) - 127));
+            const float d0 = kv_pow2(-e0), d1 = kv_pow2(-e1);  // 2^-e
+            const float vm0 = vs0 * d0, vm1 = vs1 * d1;        // the scale's mantissa
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float z[4];
+                z[0] = v0 ? sacc[nt][0] * ks0 * qfac[nt][0] + e0 : -INFINITY;
+                z[1] = v0 ? sacc[nt][1] * ks0 * qfac[nt][1] + e0 : -INFINITY;
+                z[2] = v1 ? sacc[nt][2] * ks1 * qfac[nt][0] + e1 : -INFINITY;
+                z[3] = v1 ? sacc[nt][3] * ks1 * qfac[nt][1] + e1 : -INFINITY;
+                float mx[2] = {fmaxf(z[0], z[2]), fmaxf(z[1], z[3])};
+                float alpha[2] = {1.f, 1.f};
+                // the reference moves only when a logit exceeds it by more than 2^8
+                if (__any_sync(0xffffffffu, mx[0] > m_run[nt][0] + 8.f || mx[1] > m_run[nt][1] + 8.f)) {
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 4));
+                        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 8));
+                        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 16));
+                        if (mx[x] > m_run[nt][x] + 8.f) {
+                            alpha[x] = m_run[nt][x] == -INFINITY ? 0.f : ex2_approx(m_run[nt][x] - mx[x]);
+                            m_run[nt][x] = mx[x];
+                        }
+                        l_run[nt][x] *= alpha[x];
+                    }
+#pragma unroll
+                    for (int dt = 0; dt < 8; ++dt) {
+                        o[nt][dt][0] *= alpha[0];
+                        o[nt][dt][1] *= alpha[1];
+                        o[nt][dt][2] *= alpha[0];
+                        o[nt][dt][3] *= alpha[1];
+                    }
+                }
+                const float base[2] = {m_run[nt][0] == -INFINITY ? 0.f : m_run[nt][0],
+                                       m_run[nt][1] == -INFINITY ? 0.f : m_run[nt][1]};
+                const float p0 = ex2_approx(z[0] - base[0]), p1 = ex2_approx(z[1] - base[1]);
+                const float p2 = ex2_approx(z[2] - base[0]), p3 = ex2_approx(z[3] - base[1]);
+                l_run[nt][0] += p0 * d0 + p2 * d1;
+                l_run[nt][1] += p1 * d0 + p3 * d1;
+                // P^T (keys x heads) -> B operand (keys as K, heads as N)
+                pb[nt][0] = movmatrix_trans(pack_f16x2(p0 * vm0, p1 * vm0));
+                pb[nt][1] = movmatrix_trans(pack_f16x2(p2 * vm1, p3 * vm1));
+            }
+            // O^T += V^T P^T: fragment dt's rows are dims 16 g + 2 dt and 16 g + 2 dt + 1
+            {
+                const uint8_t* p = sv + 2 * j * kKvD + ((g ^ (2 * j)) << 4);
+                const uint4 A = *reinterpret_cast<const uint4*>(p), B = *reinterpret_cast<const uint4*>(p + kKvD);
+                const uint4 E = *reinterpret_cast<const uint4*>(p + 8 * kKvD), F = *reinterpret_cast<const uint4*>(p + 9 * kKvD);
+                const uint32_t aw[4] = {A.x, A.y, A.z, A.w}, bw[4] = {B.x, B.y, B.z, B.w};
+                const uint32_t ew[4] = {E.x, E.y, E.z, E.w}, fw[4] = {F.x, F.y, F.z, F.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t x = __byte_perm(aw[w], bw[w], half ? 0x7362 : 0x5140);
+                        const uint32_t y = __byte_perm(ew[w], fw[w], half ? 0x7362 : 0x5140);
+                        const uint32_t a[4] = {kv_f16x2<FMT, false>(x), kv_f16x2<FMT, true>(x), kv_f16x2<FMT, false>(y),
+                                               kv_f16x2<FMT, true>(y)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_16816_f16(o[nt][2 * w + half], a, pb[nt][0], pb[nt][1]);
+                    }
+                }
+            }
+        }
+        st = st + 1 == S ? 0 : st + 1;
+        ++at;
+        if (--left) continue;
+
+        // ---- the row's last tile in this block: join the warps of a KV head, write
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float l = l_run[nt][x];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                l_run[nt][x] = l;
+            }
+        for (int n = nsub; n > 1;) {
+            const int h = (n + 1) / 2;
+            const bool gives = sub >= h && sub < n, takes = sub < n - h;
+            float* mine = xch + (gives ? (sub - h) * Hkv + head : sub * Hkv + head) * ((16 + 4 * NT) * 32);
+            float* ml = mine + 16 * 32;
+            float a1[NT][2], a2[NT][2];
+#pragma unroll
+            for (int ph = 0; ph < 2 * NT; ++ph) {
+                constexpr int kHalf = 4;
+                const int nt = ph >> 1, dt0 = (ph & 1) * kHalf;
+                __syncthreads();  // the area is free
+                if (gives) {
+                    if (ph == 0) {
+#pragma unroll
+                        for (int k = 0; k < NT; ++k) {
+                            ml[(4 * k) * 32 + lane] = m_run[k][0], ml[(4 * k + 1) * 32 + lane] = m_run[k][1];
+                            ml[(4 * k + 2) * 32 + lane] = l_run[k][0], ml[(4 * k + 3) * 32 + lane] = l_run[k][1];
+                        }
+                    }
+#pragma unroll
+                    for (int dt = 0; dt < kHalf; ++dt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) mine[(dt * 4 + x) * 32 + lane] = o[nt][dt0 + dt][x];
+                }
+                __syncthreads();
+                if (takes) {
+                    if (ph == 0) {
+#pragma unroll
+                        for (int k = 0; k < NT; ++k)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const float m2 = ml[(4 * k + x) * 32 + lane], l2 = ml[(4 * k + 2 + x) * 32 + lane];
+                                const float mn = fmaxf(m_run[k][x], m2), bs = mn == -INFINITY ? 0.f : mn;
+                                a1[k][x] = exp2f(m_run[k][x] - bs), a2[k][x] = exp2f(m2 - bs);
+                                l_run[k][x] = l_run[k][x] * a1[k][x] + l2 * a2[k][x];
+                                m_run[k][x] = mn;
+                            }
+                    }
+#pragma unroll
+                    for (int dt = 0; dt < kHalf; ++dt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            o[nt][dt0 + dt][x] = o[nt][dt0 + dt][x] * a1[nt][x & 1] + mine[(dt * 4 + x) * 32 + lane] * a2[nt][x & 1];
+                }
+            }
+            n = h;
+        }
+        if (sub == 0) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int hl = nt * 8 + 2 * j + x;
+                    if (hl >= G) continue;
+                    const int h = head * G + hl;
+                    if (whole) {
+                        const float inv = l_run[nt][x] == 0.f ? 0.f : 1.f / l_run[nt][x];
+                        uint32_t w[8];
+#pragma unroll
+                        for (int dt = 0; dt < 8; ++dt) w[dt] = pack_bf16x2(o[nt][dt][x] * inv, o[nt][dt][2 + x] * inv);
+                        uint4* dst = reinterpret_cast<uint4*>(P.out + ((long long)row * P.Hq + h) * kKvD + 16 * g);
+                        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        if (P.lse && g == 0)
+                            P.lse[(long long)row * P.Hq + h] =
+                                l_run[nt][x] == 0.f ? -INFINITY : (m_run[nt][x] + log2f(l_run[nt][x])) * 0.69314718055994531f;
+                    } else {
+                        float* part = P.part + ((2ll * blockIdx.x + (first_part ? 0 : 1)) * P.Hq + h) * kPagedPartStride;
+                        float4* dst = reinterpret_cast<float4*>(part + 16 * g);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            dst[w] = make_float4(o[nt][2 * w][x], o[nt][2 * w][2 + x], o[nt][2 * w + 1][x], o[nt][2 * w + 1][2 + x]);
+                        if (g == 0) part[kKvD] = m_run[nt][x], part[kKvD + 1] = l_run[nt][x];
+                    }
+                }
+        }
+        first_part = false;
+        if (i + 1 < tiles) {
+            int b, n;
+            do paged_row(P, ++row, b, n);
+            while (paged_count(P, n) == 0);
+            begin_row(0);
+        }
+    }
+}
+
+constexpr int kCombineThreads = 256;
+
+// Joins the parts of the rows that several blocks shared, and writes the rows without keys.  A block has
+// 8 / WPH heads of a row at a time, WPH warps on each, which take the parts in turn.
+template <int WPH>
+__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const PagedParams P, int TK) {
+    constexpr int HB = 8 / WPH;
+    __shared__ float s_l[8];
+    __shared__ float4 s_o[8][32];
+    const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int hs = warp / WPH, pw = warp % WPH;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     int b, n;
     paged_row(P, t, b, n);
-    const int count = P.idx ? min(P.topk, n) : n;
-    float q[kPagedMaxG][4], o[kPagedMaxG][4], m[kPagedMaxG], l[kPagedMaxG];
+    const int nt = (paged_count(P, n) + TK - 1) / TK;
+    const long long start = P.row_start[t], chunk = P.row_start[P.T];
+    const long long c0 = start / chunk, c1 = nt ? (start + nt - 1) / chunk : c0;
+    if (nt && c0 == c1) return;  // one block held the row and wrote it
+    const int parts = nt ? (int)(c1 - c0) + 1 : 0;
+    for (int h0 = blockIdx.y * HB; h0 < P.Hq; h0 += gridDim.y * HB) {
+        const int h = h0 + hs;
+        const bool any = h < P.Hq;
+        // part p: of block c0 + p, its slot 0 where the row reaches back to or before the block's first tile
+        auto at = [&](int p) {
+            const long long c = c0 + p;
+            return P.part + ((2 * c + (start <= c * chunk ? 0 : 1)) * P.Hq + h) * kPagedPartStride;
+        };
+        float mx = -INFINITY;
+        if (any)
+            for (int p = lane; p < parts; p += 32) mx = fmaxf(mx, at(p)[kKvD]);
 #pragma unroll
-    for (int h = 0; h < kPagedMaxG; ++h) {
-        m[h] = -INFINITY, l[h] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            o[h][i] = 0.f;
-            q[h][i] = h < G ? __bfloat162float(P.q[((long long)t * P.Hq + g * G + h) * kKvD + lane * 4 + i]) : 0.f;
+        for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+        const float bs = mx == -INFINITY ? 0.f : mx;
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (any) {
+#pragma unroll 8
+            for (int p = pw; p < parts; p += WPH) {
+                const float* src = at(p);
+                const float2 ml = *reinterpret_cast<const float2*>(src + kKvD);
+                const float4 v = *reinterpret_cast<const float4*>(src + lane * 4);
+                const float w = exp2f(ml.x - bs);
+                l += ml.y * w;
+                acc.x += v.x * w, acc.y += v.y * w, acc.z += v.z * w, acc.w += v.w * w;
+            }
         }
-    }
-    for (int e = warp; e < count; e += 4) {
-        const int key = P.idx ? P.idx[(long long)t * P.topk + e] : e;
-        if (key < 0 || key >= n) continue;
-        const int pid = P.table[(long long)b * P.max_pages + (key >> P.page_shift)];
-        if (pid < 0 || pid >= P.num_pages) {
-            record_error(DSA_DEV_ERR_BOUNDS, 0xb02);
-            continue;
+        if (WPH > 1) {
+            __syncthreads();
+            s_o[warp][lane] = acc;
+            if (lane == 0) s_l[warp] = l;
+            __syncthreads();
+            if (pw == 0) {
+#pragma unroll
+                for (int w = 1; w < WPH; ++w) {
+                    const float4 v = s_o[warp + w][lane];
+                    l += s_l[warp + w];
+                    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+                }
+            }
         }
-        const long long slot = ((long long)pid << P.page_shift) + (key & ((1 << P.page_shift) - 1));
-        const long long at = (slot * P.Hkv + g) * kKvD + lane * 4;
-        float k[4], v[4];
-        kv_value4<FMT>(*reinterpret_cast<const uint32_t*>(P.k_pages + at), k);
-        kv_value4<FMT>(*reinterpret_cast<const uint32_t*>(P.v_pages + at), v);
-        const float ks = P.k_scale[(long long)pid * P.Hkv + g] * P.scale_log2;
-        const float vs = P.v_scale[(long long)pid * P.Hkv + g];
-#pragma unroll
-        for (int h = 0; h < kPagedMaxG; ++h) {
-            if (h >= G) break;
-            float z = q[h][0] * k[0] + q[h][1] * k[1] + q[h][2] * k[2] + q[h][3] * k[3];
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-            z *= ks;
-            const float mn = fmaxf(m[h], z), a = exp2f(m[h] - mn), p = exp2f(z - mn);
-            m[h] = mn, l[h] = l[h] * a + p;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[h][i] = o[h][i] * a + p * v[i] * vs;
+        if (pw == 0 && any) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            uint2 w;
+            w.x = pack_bf16x2(acc.x * inv, acc.y * inv), w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(P.out + ((long long)t * P.Hq + h) * kKvD + lane * 4) = w;
+            if (P.lse && lane == 0)
+                P.lse[(long long)t * P.Hq + h] = l == 0.f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994531f;
         }
-    }
-#pragma unroll
-    for (int h = 0; h < kPagedMaxG; ++h) {
-        if (h >= G) break;
-        if (lane == 0) sm[warp][h] = m[h], sl[warp][h] = l[h];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) so[warp][h][lane * 4 + i] = o[h][i];
-    }
-    __syncthreads();
-    for (int h = warp; h < G; h += 4) {
-        float mx = -INFINITY, sum = 0.f, acc[4] = {};
-        for (int w = 0; w < 4; ++w) mx = fmaxf(mx, sm[w][h]);
-        for (int w = 0; w < 4; ++w) {
-            const float a = sm[w][h] == -INFINITY ? 0.f : exp2f(sm[w][h] - mx);
-            sum += sl[w][h] * a;
-            for (int i = 0; i < 4; ++i) acc[i] += so[w][h][lane * 4 + i] * a;
-        }
-        const long long row = (long long)t * P.Hq + g * G + h;
-        for (int i = 0; i < 4; ++i)
-            P.out[row * kKvD + lane * 4 + i] = __float2bfloat16_rn(count && mx != -INFINITY ? acc[i] / sum : 0.f);
-        if (P.lse && lane == 0) P.lse[row] = mx == -INFINITY ? -INFINITY : (mx + log2f(sum)) * 0.69314718055994531f;
     }
 }
 

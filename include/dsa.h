@@ -313,7 +313,7 @@ dsa_status dsa_rope_freqs(int rot_dim, double theta, int scaling, double factor,
  * reported by dsa_sync_status() as DSA_ERR_DEVICE_INPUT, as are a ctx_len or cu_new out of range
  * (that sequence is skipped) and a page number outside [0, num_pages) (that page is skipped).
  * Supported: D = 128, Hkv in {1, 2, 4}, page_size in {16, 32, 64, 128}, rot_dim a multiple of 16 up to
- * 128, N < 2^30, B < 2^29, max_pages * page_size < 2^31.
+ * 128, N < 2^30, B < 2^29, max_pages * page_size <= 2^30.
  */
 dsa_status dsa_kv_append(const void *k_new, const void *v_new, int64_t k_ts, int64_t k_hs, int64_t v_ts, int64_t v_hs,
                          int64_t N, const int32_t *cu_new, const int32_t *ctx_len, const int32_t *rope_pos,
@@ -340,7 +340,7 @@ dsa_status dsa_kv_append(const void *k_new, const void *v_new, int64_t k_ts, int
  * A row whose seq or n_keys is out of range counts as empty and a key whose page number is outside
  * [0, num_pages) is skipped; dsa_sync_status() reports both as DSA_ERR_DEVICE_INPUT.
  * Supported: D = 128, Hkv in {1, 2, 4}, Hq / Hkv <= 16, page_size in {16, 32, 64, 128}, topk <= 65536,
- * max_pages * page_size < 2^31.
+ * max_pages * page_size <= 2^30, num_pages * page_size < 2^31, scales up to 2^120 in size.
  */
 dsa_status dsa_paged_attn(const void *q, const void *k_pages, const void *v_pages, const float *k_scale,
                           const float *v_scale, const int32_t *page_table, const int32_t *seq, const int32_t *n_keys,

@@ -135,6 +135,19 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_fast = None
+
+
+def _native():
+    """The marshalling module: the checks below and the C call in one step, for operands that need no error
+    message (None otherwise).  Loaded with the first call that uses it, since it needs torch."""
+    global _fast
+    import torch  # noqa: F401
+    from . import _marshal
+    _fast = _marshal
+    return _fast
+
+
 def _need(t, dtype, name, shape):
     """One tensor argument: its type, dtype, shape (None: any extent) and contiguity.  The
     library reads every size from the leading operand, so an operand whose shape disagrees would
@@ -385,6 +398,10 @@ def rope_freqs(rot_dim: int, theta: float = 10000.0, scaling: str = "plain", fac
 def dsa_rope(x, out, inv_freq, pos=None, pos0: int = 0, rot_offset: int = 0, interleaved: bool = False,
              mscale: float = 1.0, inverse: bool = False, stream=None) -> None:
     """Rotary positions of x's heads into out (which may be x); inverse gives the gradient of the same."""
+    if stream is None:
+        st = (_fast or _native()).rope(x, out, inv_freq, pos, pos0, rot_offset, interleaved, mscale, inverse)
+        if st is not None:
+            return _check(st, "dsa_rope")
     import torch
     if getattr(x, "dtype", None) not in (torch.bfloat16, torch.float32):
         raise TypeError(f"x must be a bfloat16 or float32 tensor, got {getattr(x, 'dtype', type(x))}")
@@ -420,6 +437,11 @@ def dsa_kv_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, page_table, 
                   rope_pos=None, rot_offset: int = 0, interleaved: bool = False, mscale: float = 1.0,
                   stream=None) -> None:
     """Append tokens to a paged 8-bit cache at positions ctx_len[b].., keys rotated where inv_freq is given."""
+    if stream is None:
+        st = (_fast or _native()).kv_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, page_table, ctx_len,
+                                               cu_new, inv_freq, rope_pos, rot_offset, interleaved, mscale)
+        if st is not None:
+            return _check(st, "dsa_kv_append")
     import torch
     fmt, num_pages, page, Hkv, D, B, max_pages = _cache_operands(k_pages, v_pages, k_scale, v_scale, page_table)
     k_ts, k_hs = _heads(k_new, torch.bfloat16, "k_new", (None, Hkv, D))
@@ -449,6 +471,11 @@ def dsa_paged_attn(q, k_pages, v_pages, k_scale, v_scale, page_table, n_keys, sc
                    lse=None, ws=None, stream=None) -> None:
     """Attention of q's rows over a paged 8-bit cache: the first n_keys[t] keys of each row's sequence, or
     those of them that idx names."""
+    if stream is None:
+        st = (_fast or _native()).paged_attn(q, k_pages, v_pages, k_scale, v_scale, page_table, n_keys, scale, out, seq,
+                                                idx, lse, ws)
+        if st is not None:
+            return _check(st, "dsa_paged_attn")
     import torch
     bf = torch.bfloat16
     fmt, num_pages, page, Hkv, D, B, max_pages = _cache_operands(k_pages, v_pages, k_scale, v_scale, page_table)

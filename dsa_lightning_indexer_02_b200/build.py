@@ -1,4 +1,5 @@
-"""Build libdsa.so (sm_100a) in-tree with nvcc.  No GPU is needed to build."""
+"""Build libdsa.so (sm_100a) in-tree with nvcc, and with the host compiler the binding's marshalling module
+_marshal.so, which links it.  No GPU is needed to build."""
 from __future__ import annotations
 
 import os
@@ -12,7 +13,10 @@ LIB = os.path.join(HERE, "libdsa.so")
 DEPS = [os.path.join(HERE, "csrc", f) for f in (
     "dsa_lib.cu", "ptx.cuh", "indexer.cuh", "topk.cuh", "attn.cuh", "attn_dedup.cuh", "kl.cuh", "rope.cuh",
     "kv8.cuh", "paged_attn.cuh")]
-DEPS.append(os.path.join(ROOT, "include", "dsa.h"))
+DEPS += [os.path.join(ROOT, "include", "dsa.h"), os.path.abspath(__file__)]
+
+MARSHAL_SRC = os.path.join(HERE, "csrc", "marshal.cpp")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v", "--expt-relaxed-constexpr"]
@@ -32,10 +36,38 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in DEPS)
 
 
+def build_marshal(force: bool = False) -> str:
+    """The marshalling module, against the running interpreter's and torch's headers."""
+    deps = (MARSHAL_SRC, os.path.join(ROOT, "include", "dsa.h"))
+    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL) for d in deps):
+        return MARSHAL
+    import sysconfig
+    import torch
+    top = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"], "-isystem", f"{top}/include",
+           "-isystem", f"{top}/include/torch/csrc/api/include", "-isystem", f"{cuda}/include", MARSHAL_SRC,
+           "-o", MARSHAL + ".tmp", LIB, f"-L{top}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{top}/lib"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("the host compiler failed building _marshal.so")
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    lib = build_lib(force, verbose)
+    build_marshal(force)
+    return lib
+
+
+def build_lib(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
-    cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), SRC, "-o", LIB + ".tmp"]
+    cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), SRC, "-Xlinker", "-soname=libdsa.so", "-o", LIB + ".tmp"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)

@@ -537,10 +537,10 @@ cudaError_t launch_combine_t(const PagedParams& P, int TK, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, paged_combine_kernel<WPH>, P, TK);
 }
 
-template <int FMT, int NT>
+template <int FMT, int NT, int HKV, bool IDX>
 dsa_status launch_paged_t(PagedParams P, cudaStream_t s) {
     using C = PagedCfg<NT>;
-    auto kern = paged_attn_kernel<FMT, NT>;
+    auto kern = paged_attn_kernel<FMT, NT, HKV, IDX>;
     static DeviceFlags attr_set;
     if (!set_smem_limit(kern, C::SMEM, attr_set)) return DSA_ERR_CUDA;
     const int sms = num_sms();
@@ -555,19 +555,29 @@ dsa_status launch_paged_t(PagedParams P, cudaStream_t s) {
     }
     // 8 warps on a head while there are few (row, head) pairs, down to one
     LaunchScope ls(K_COMBINE, s);
-    const int TK = 16 * C::NW / P.Hkv, pairs = P.T * P.Hq;
+    const int TK = C::NW / HKV * C::KT * 16, pairs = P.T * P.Hq;
     const cudaError_t e = pairs <= 1184 ? launch_combine_t<8>(P, TK, s)
                           : pairs <= 2368 ? launch_combine_t<4>(P, TK, s)
                           : pairs <= 4736 ? launch_combine_t<2>(P, TK, s) : launch_combine_t<1>(P, TK, s);
     return e == cudaSuccess ? launch_status() : DSA_ERR_CUDA;
 }
 
+template <int FMT, int NT>
+dsa_status launch_paged(const PagedParams& P, cudaStream_t s) {
+    switch (P.Hkv) {
+    case 1: return P.idx ? launch_paged_t<FMT, NT, 1, true>(P, s) : launch_paged_t<FMT, NT, 1, false>(P, s);
+    case 2: return P.idx ? launch_paged_t<FMT, NT, 2, true>(P, s) : launch_paged_t<FMT, NT, 2, false>(P, s);
+    case 4: return P.idx ? launch_paged_t<FMT, NT, 4, true>(P, s) : launch_paged_t<FMT, NT, 4, false>(P, s);
+    }
+    return DSA_ERR_UNSUPPORTED;
+}
+
 dsa_status run_paged_attn(PagedParams P, int fmt, void* ws, cudaStream_t s) {
     P.part = static_cast<float*>(ws);
     P.row_start = reinterpret_cast<long long*>(static_cast<uint8_t*>(ws) + paged_part_bytes(P.Hq));
     const bool two = P.Hq / P.Hkv > 8;
-    if (fmt == DSA_KV_E4M3) return two ? launch_paged_t<KV_E4M3, 2>(P, s) : launch_paged_t<KV_E4M3, 1>(P, s);
-    return two ? launch_paged_t<KV_INT8, 2>(P, s) : launch_paged_t<KV_INT8, 1>(P, s);
+    if (fmt == DSA_KV_E4M3) return two ? launch_paged<KV_E4M3, 2>(P, s) : launch_paged<KV_E4M3, 1>(P, s);
+    return two ? launch_paged<KV_INT8, 2>(P, s) : launch_paged<KV_INT8, 1>(P, s);
 }
 
 // ------------------------------------------------------------------ decode helpers

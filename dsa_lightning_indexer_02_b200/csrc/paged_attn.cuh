@@ -48,20 +48,22 @@ struct PagedParams {
     long long* row_start;              // [T + 1]: the rows' first tiles, and the tiles of a block behind them
 };
 
-// NT: groups of 8 query heads of a KV head.  One group leaves registers for two blocks of 8 warps on an
-// SM; two groups take one block of 12.
+// NT: groups of 8 query heads of a KV head.  KT: 16-key tiles of a warp's step.
 template <int NT>
 struct PagedCfg {
-    static constexpr int NW = NT == 1 ? 8 : 12;
-    static constexpr int S = NT == 1 ? 3 : 4;  // ring stages of a warp
+    static constexpr int KT = 2;
+    static constexpr int NW = 12;
+    static constexpr int S = 2;  // ring stages of a warp
+    static constexpr int CTAS = 1;
     static constexpr int THREADS = NW * 32;
-    static constexpr int CTAS = NT == 1 ? 2 : 1;
-    static constexpr int STAGE = 2 * 16 * kKvD;  // K rows, V rows
-    static constexpr int RING = NW * S * STAGE;
-    static constexpr int META = NW * S * (32 + 4) * 4;  // scales of 16 keys (K, V), mask, pad
-    static constexpr int XCH = (NW / 2) * (16 + 4 * NT) * 32 * 4;
-    static constexpr int SMEM = RING + META + XCH;
+    static constexpr int STAGE = KT * 2 * 16 * kKvD;  // K rows, V rows
+    static constexpr int META = 68;                   // floats of a stage: K's and V's scales, mask
+    static constexpr int RING_BYTES = NW * S * STAGE;
+    static constexpr int META_BYTES = NW * S * META * 4;
+    static constexpr int XCH_BYTES = (NW / 2) * (16 + 4 * NT) * 32 * 4;
+    static constexpr int SMEM = RING_BYTES + META_BYTES + XCH_BYTES;
 };
+constexpr float kPagedNone = -1e30f;  // the running maximum before any key
 
 // Sequence and key count of row t; a bad one is reported and leaves the row empty.
 __device__ __forceinline__ void paged_row(const PagedParams& P, int t, int& b, int& n) {
@@ -105,15 +107,18 @@ __device__ __forceinline__ uint32_t kv_f16x2(uint32_t w) {
     }
 }
 
-template <int FMT, int NT>
+// IDX: keys named by idx; otherwise a step's 16 keys lie side by side in one page.
+template <int FMT, int NT, int HKV, bool IDX>
 __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) paged_attn_kernel(const PagedParams P) {
     using C = PagedCfg<NT>;
-    constexpr int NW = C::NW, S = C::S;
+    constexpr int NW = C::NW, S = C::S, KT = C::KT;
+    constexpr int NSUB = NW / HKV;        // warps of a KV head
+    constexpr int TK = NSUB * KT * 16;    // keys of a tile
+    constexpr int ROWB = HKV * kKvD;      // bytes between a page's tokens
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int Hkv = P.Hkv, G = P.Hq / Hkv;
-    const int head = warp % Hkv, sub = warp / Hkv, nsub = NW / Hkv;
-    const int TK = 16 * nsub;  // keys of a tile
+    const int G = P.Hq / HKV;
+    const int head = warp % HKV, sub = warp / HKV;
     const int g = lane >> 2, j = lane & 3;
 
     // ---- this block's tiles [w0, w1), from tile `tile0` of row `row0` on
@@ -183,25 +188,28 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     const int tiles = (int)(w1 - w0);
 
     uint8_t* ring = smem + warp * (S * C::STAGE);
-    float* meta = reinterpret_cast<float*>(smem + C::RING) + warp * (S * 36);
-    float* xch = reinterpret_cast<float*>(smem + C::RING + C::META);
+    float* meta = reinterpret_cast<float*>(smem + C::RING_BYTES) + warp * (S * C::META);
+    float* xch = reinterpret_cast<float*>(smem + C::RING_BYTES + C::META_BYTES);
 
-    // ---- copies.  A tile passes three steps, one iteration apart: its keys' numbers are loaded (lane
-    // i < 16: key i of this warp), their pages looked up, their rows copied.
+    // ---- copies.  A step's keys pass three stages, one iteration apart: their numbers are loaded, their
+    // pages looked up, their rows copied.  With IDX lane i has key i of the step (KT = 1: i mod 16);
+    // otherwise lane i has the first key of 16-key tile i mod 16, for i mod 16 < KT.
     int f_row = row0, f_tile = tile0, f_nt = 0, f_b = 0, f_n = 0, f_left = tiles;  // front cursor
     if (tiles > 0) {
         paged_row(P, f_row, f_b, f_n);
         f_nt = (paged_count(P, f_n) + TK - 1) / TK;
     }
-    int a_key = -1, a_n = 0, a_b = 0;  // key numbers loaded
-    int b_off = 0, b_pid = -1;         // pages looked up: -1 none
+    const int my_key = IDX ? (KT == 2 ? lane : lane & 15) : (lane & 15) * 16;
+    const bool has_key = IDX || (lane & 15) < KT;
+    int a_key = -1, a_n = 0, a_b = 0;  // numbers loaded
+    int b_slot = -1, b_valid = 0;      // pages looked up: token's slot in the pool, -1 none; keys from it on
     auto load_keys = [&]() {
         a_key = -1;
         if (f_left <= 0) return;
         --f_left;
-        const int e = f_tile * TK + sub * 16 + lane;
+        const int e = f_tile * TK + sub * (KT * 16) + my_key;
         a_n = f_n, a_b = f_b;
-        if (lane < 16 && e < paged_count(P, f_n)) a_key = P.idx ? P.idx[(long long)f_row * P.topk + e] : e;
+        if (has_key && e < paged_count(P, f_n)) a_key = IDX ? P.idx[(long long)f_row * P.topk + e] : e;
         if (++f_tile == f_nt && f_left > 0) {
             do {
                 paged_row(P, ++f_row, f_b, f_n);
@@ -211,35 +219,67 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         }
     };
     auto look_up = [&]() {
-        b_pid = -1;
+        b_slot = -1, b_valid = 0;
         if (a_key >= 0 && a_key < a_n) {
-            b_pid = P.table[(long long)a_b * P.max_pages + (a_key >> P.page_shift)];
-            b_off = a_key & ((1 << P.page_shift) - 1);
-            if (b_pid < 0 || b_pid >= P.num_pages) {
+            const int pid = P.table[(long long)a_b * P.max_pages + (a_key >> P.page_shift)];
+            if (pid < 0 || pid >= P.num_pages) {
                 record_error(DSA_DEV_ERR_BOUNDS, 0xb02);
-                b_pid = -1;
+            } else {
+                b_slot = (pid << P.page_shift) + (a_key & ((1 << P.page_shift) - 1));
+                b_valid = min(16, a_n - a_key);
             }
         }
     };
+    // lane's part of every row copy: row lane / 8 of four, 16-byte chunk lane % 8
+    const uint8_t* k_lane = P.k_pages + head * kKvD + (lane & 7) * 16 + (IDX ? 0 : (lane >> 3) * ROWB);
+    const uint8_t* v_lane = P.v_pages + head * kKvD + (lane & 7) * 16 + (IDX ? 0 : (lane >> 3) * ROWB);
+    const int lr = lane >> 3, lc = lane & 7;
     auto copy_rows = [&](int st) {
-        const unsigned mask = __ballot_sync(0xffffffffu, b_pid >= 0);
-        float* sc = meta + st * 36;
-        if (lane == 0) reinterpret_cast<unsigned*>(sc)[32] = mask;
-        if (mask) {
-            uint8_t* dst = ring + st * C::STAGE;
-            const int slot = (b_pid << P.page_shift) + b_off;
+        float* sc = meta + st * C::META;
+        uint8_t* dst = ring + st * C::STAGE + lr * kKvD;
+        // row r = 4 i + lr of a tile: K's chunk c goes to c ^ 4 (r & 1), V's to c ^ (r & 6)
+        const int k_at = (lc ^ ((lr & 1) << 2)) << 4;
+        if constexpr (IDX) {
+            const unsigned mask = __ballot_sync(0xffffffffu, b_slot >= 0);
+            if (lane == 0) reinterpret_cast<unsigned*>(sc)[C::META - 1] = mask;
+            if (mask) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = i * 4 + (lane >> 3), c = lane & 7;
-                const int s = __shfl_sync(0xffffffffu, slot, r);
-                const bool ok = mask >> r & 1;
-                const long long at = ok ? ((long long)s * Hkv + head) * kKvD + c * 16 : 0;
-                cp_async_16(dst + r * kKvD + ((c ^ ((r & 1) << 2)) << 4), P.k_pages + at, ok);
-                cp_async_16(dst + 16 * kKvD + r * kKvD + ((c ^ (r & 6)) << 4), P.v_pages + at, ok);
+                for (int i = 0; i < 4 * KT; ++i) {
+                    const int r = i * 4 + lr;
+                    const int s = __shfl_sync(0xffffffffu, b_slot, r);
+                    const bool ok = s >= 0;
+                    const long long at = ok ? (long long)s * ROWB : 0;
+                    const int v_at = (lc ^ (((i & 1) << 2) | (lr & 2))) << 4;
+                    cp_async_16(dst + (i >> 2) * 4096 + (i & 3) * 512 + k_at, k_lane + at, ok);
+                    cp_async_16(dst + (i >> 2) * 4096 + 2048 + (i & 3) * 512 + v_at, v_lane + at, ok);
+                }
+                const bool ok = b_slot >= 0;
+                const long long at = ok ? (long long)(b_slot >> P.page_shift) * HKV + head : 0;
+                if (KT == 2) {
+                    cp_async_4(sc + lane, P.k_scale + at, ok);
+                    cp_async_4(sc + 32 + lane, P.v_scale + at, ok);
+                } else {
+                    cp_async_4(sc + (lane & 15) + (lane & 16) * 2, (lane < 16 ? P.k_scale : P.v_scale) + at, ok);
+                }
             }
-            const int pid = __shfl_sync(0xffffffffu, b_pid, lane & 15);
-            const bool ok = mask >> (lane & 15) & 1;
-            cp_async_4(sc + lane, (lane < 16 ? P.k_scale : P.v_scale) + (ok ? (long long)pid * Hkv + head : 0), ok);
+        } else {
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                const int s = __shfl_sync(0xffffffffu, b_slot, t), n = __shfl_sync(0xffffffffu, b_valid, t);
+                if (lane == 0) reinterpret_cast<int*>(sc)[C::META - 1 - t] = n;
+                if (n == 0) continue;
+                const long long at = (long long)s * ROWB;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool ok = n == 16 || i * 4 + lr < n;
+                    const int v_at = (lc ^ (((i & 1) << 2) | (lr & 2))) << 4;
+                    cp_async_16(dst + t * 4096 + i * 512 + k_at, k_lane + at + i * 4 * ROWB, ok);
+                    cp_async_16(dst + t * 4096 + 2048 + i * 512 + v_at, v_lane + at + i * 4 * ROWB, ok);
+                }
+            }
+            if (has_key && b_valid)
+                cp_async_4(sc + (lane & 15) * 2 + (lane >> 4),
+                           (lane < 16 ? P.k_scale : P.v_scale) + (long long)(b_slot >> P.page_shift) * HKV + head, true);
         }
         cp_async_commit();
     };
@@ -295,7 +335,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
                 qfac[nt8][jj] = __shfl_sync(0xffffffffu, fac, (2 * j + jj) * 4);
-                m_run[nt8][jj] = -INFINITY, l_run[nt8][jj] = 0.f;
+                m_run[nt8][jj] = kPagedNone, l_run[nt8][jj] = 0.f;
             }
 #pragma unroll
             for (int dt = 0; dt < 8; ++dt)
@@ -311,23 +351,30 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         copy_rows(st == 0 ? S - 1 : st - 1);  // the stage that the last iteration used up
         look_up();
         load_keys();
-        const float* sc = meta + st * 36;
-        const unsigned mask = reinterpret_cast<const unsigned*>(sc)[32];
-        if (mask) {
-            const uint8_t* sk = ring + st * C::STAGE;
-            const uint8_t* sv = sk + 16 * kKvD;
+        const float* sc = meta + st * C::META;
+        int valid[KT];      // dense: keys of each tile;  IDX: the tile's bits of the mask
+        bool some = false;  // any key at all
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+            if constexpr (IDX) valid[t] = reinterpret_cast<const unsigned*>(sc)[C::META - 1] >> (16 * t) & 0xffffu;
+            else valid[t] = reinterpret_cast<const int*>(sc)[C::META - 1 - t];
+            some |= valid[t] != 0;
+        }
+        if (some) {
+            const uint8_t* stage = ring + st * C::STAGE;
             // S^T: rows are keys g and g + 8; the dims of step kk are word kk of the thread's two chunks
-            float sacc[NT][4];
+            float z[KT][NT][4];
+            const uint8_t* k0 = stage + g * kKvD + ((j ^ ((g & 1) << 2)) << 4);
+            const uint8_t* k1 = stage + g * kKvD + ((j ^ ((g & 1) << 2) ^ 4) << 4);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int t = 0; t < KT; ++t) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) sacc[nt][x] = 0.f;
-            {
-                const uint8_t* k0 = sk + g * kKvD + ((j ^ ((g & 1) << 2)) << 4);
-                const uint8_t* k1 = sk + g * kKvD + ((j ^ ((g & 1) << 2) ^ 4) << 4);
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) z[t][nt][x] = 0.f;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const uint8_t* p = half ? k1 : k0;
+                    const uint8_t* p = (half ? k1 : k0) + t * 4096;
                     const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 8 * kKvD);
                     const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -336,35 +383,66 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                                                kv_f16x2<FMT, true>(xw[w]), kv_f16x2<FMT, true>(yw[w])};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma_16816_f16(sacc[nt], a, qf[nt][half * 4 + w][0], qf[nt][half * 4 + w][1]);
+                            mma_16816_f16(z[t][nt], a, qf[nt][half * 4 + w][0], qf[nt][half * 4 + w][1]);
                     }
                 }
             }
-            const bool v0 = mask >> g & 1, v1 = mask >> (g + 8) & 1;
-            const float ks0 = sc[g], ks1 = sc[g + 8], vs0 = sc[16 + g], vs1 = sc[24 + g];
-            const int e0 = min(120, max(-80, (int)(__float_as_uint(vs0) >> 23 & 255u) - 127));
-            const int e1 = min(120, max(-80, (int)(__float_as_uint(vs1) >> 23 & 255u) - 127));
-            const float d0 = kv_pow2(-e0), d1 = kv_pow2(-e1);  // 2^-e
-            const float vm0 = vs0 * d0, vm1 = vs1 * d1;        // the scale's mantissa
-            uint32_t pb[NT][2];
+            // logits in log2 plus V's exponent; d = 2^-e, vm = V's scale * d
+            float d[KT][2], vm[KT][2];
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                float ks[2], vs[2];
+                if constexpr (IDX) {
+                    ks[0] = sc[16 * t + g], ks[1] = sc[16 * t + 8 + g];
+                    vs[0] = sc[32 + 16 * t + g], vs[1] = sc[32 + 16 * t + 8 + g];
+                } else {
+                    const float2 kv = *reinterpret_cast<const float2*>(sc + 2 * t);
+                    ks[0] = ks[1] = kv.x, vs[0] = vs[1] = kv.y;
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int e = min(120, max(-80, (int)(__float_as_uint(vs[y]) >> 23 & 255u) - 127));
+                    d[t][y] = kv_pow2(-e);
+                    vm[t][y] = vs[y] * d[t][y];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            z[t][nt][2 * y + x] = fmaf(z[t][nt][2 * y + x], ks[y] * qfac[nt][x], (float)e);
+                }
+                if (valid[t] != (IDX ? 0xffff : 16)) {
+                    const bool v0 = IDX ? valid[t] >> g & 1 : g < valid[t], v1 = IDX ? valid[t] >> (g + 8) & 1 : g + 8 < valid[t];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            if (!v0) z[t][nt][x] = -INFINITY;
+                            if (!v1) z[t][nt][2 + x] = -INFINITY;
+                        }
+                    if (!v0) d[t][0] = 0.f, vm[t][0] = 0.f;  // whatever an uncopied stage holds
+                    if (!v1) d[t][1] = 0.f, vm[t][1] = 0.f;
+                }
+            }
+            uint32_t pb[KT][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float z[4];
-                z[0] = v0 ? sacc[nt][0] * ks0 * qfac[nt][0] + e0 : -INFINITY;
-                z[1] = v0 ? sacc[nt][1] * ks0 * qfac[nt][1] + e0 : -INFINITY;
-                z[2] = v1 ? sacc[nt][2] * ks1 * qfac[nt][0] + e1 : -INFINITY;
-                z[3] = v1 ? sacc[nt][3] * ks1 * qfac[nt][1] + e1 : -INFINITY;
-                float mx[2] = {fmaxf(z[0], z[2]), fmaxf(z[1], z[3])};
-                float alpha[2] = {1.f, 1.f};
+                float mx[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    mx[x] = fmaxf(z[0][nt][x], z[0][nt][2 + x]);
+#pragma unroll
+                    for (int t = 1; t < KT; ++t) mx[x] = fmaxf(mx[x], fmaxf(z[t][nt][x], z[t][nt][2 + x]));
+                }
                 // the reference moves only when a logit exceeds it by more than 2^8
                 if (__any_sync(0xffffffffu, mx[0] > m_run[nt][0] + 8.f || mx[1] > m_run[nt][1] + 8.f)) {
+                    float alpha[2] = {1.f, 1.f};
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 4));
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 8));
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 16));
                         if (mx[x] > m_run[nt][x] + 8.f) {
-                            alpha[x] = m_run[nt][x] == -INFINITY ? 0.f : ex2_approx(m_run[nt][x] - mx[x]);
+                            alpha[x] = ex2_approx(m_run[nt][x] - mx[x]);
                             m_run[nt][x] = mx[x];
                         }
                         l_run[nt][x] *= alpha[x];
@@ -377,19 +455,23 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                         o[nt][dt][3] *= alpha[1];
                     }
                 }
-                const float base[2] = {m_run[nt][0] == -INFINITY ? 0.f : m_run[nt][0],
-                                       m_run[nt][1] == -INFINITY ? 0.f : m_run[nt][1]};
-                const float p0 = ex2_approx(z[0] - base[0]), p1 = ex2_approx(z[1] - base[1]);
-                const float p2 = ex2_approx(z[2] - base[0]), p3 = ex2_approx(z[3] - base[1]);
-                l_run[nt][0] += p0 * d0 + p2 * d1;
-                l_run[nt][1] += p1 * d0 + p3 * d1;
-                // P^T (keys x heads) -> B operand (keys as K, heads as N)
-                pb[nt][0] = movmatrix_trans(pack_f16x2(p0 * vm0, p1 * vm0));
-                pb[nt][1] = movmatrix_trans(pack_f16x2(p2 * vm1, p3 * vm1));
+#pragma unroll
+                for (int t = 0; t < KT; ++t) {
+                    float p[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) p[x] = ex2_approx(z[t][nt][x] - m_run[nt][x & 1]);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) l_run[nt][x] = fmaf(p[2 + x], d[t][1], fmaf(p[x], d[t][0], l_run[nt][x]));
+                    // P^T (keys x heads) -> B operand (keys as K, heads as N)
+                    pb[t][nt][0] = movmatrix_trans(pack_f16x2(p[0] * vm[t][0], p[1] * vm[t][0]));
+                    pb[t][nt][1] = movmatrix_trans(pack_f16x2(p[2] * vm[t][1], p[3] * vm[t][1]));
+                }
             }
             // O^T += V^T P^T: fragment dt's rows are dims 16 g + 2 dt and 16 g + 2 dt + 1
-            {
-                const uint8_t* p = sv + 2 * j * kKvD + ((g ^ (2 * j)) << 4);
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                if (!valid[t]) continue;  // nothing copied
+                const uint8_t* p = stage + t * 4096 + 2048 + 2 * j * kKvD + ((g ^ (2 * j)) << 4);
                 const uint4 A = *reinterpret_cast<const uint4*>(p), B = *reinterpret_cast<const uint4*>(p + kKvD);
                 const uint4 E = *reinterpret_cast<const uint4*>(p + 8 * kKvD), F = *reinterpret_cast<const uint4*>(p + 9 * kKvD);
                 const uint32_t aw[4] = {A.x, A.y, A.z, A.w}, bw[4] = {B.x, B.y, B.z, B.w};
@@ -403,7 +485,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                         const uint32_t a[4] = {kv_f16x2<FMT, false>(x), kv_f16x2<FMT, true>(x), kv_f16x2<FMT, false>(y),
                                                kv_f16x2<FMT, true>(y)};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_16816_f16(o[nt][2 * w + half], a, pb[nt][0], pb[nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) mma_16816_f16(o[nt][2 * w + half], a, pb[t][nt][0], pb[t][nt][1]);
                     }
                 }
             }
@@ -423,10 +505,10 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 l_run[nt][x] = l;
             }
-        for (int n = nsub; n > 1;) {
+        for (int n = NSUB; n > 1;) {
             const int h = (n + 1) / 2;
             const bool gives = sub >= h && sub < n, takes = sub < n - h;
-            float* mine = xch + (gives ? (sub - h) * Hkv + head : sub * Hkv + head) * ((16 + 4 * NT) * 32);
+            float* mine = xch + (gives ? (sub - h) * HKV + head : sub * HKV + head) * ((16 + 4 * NT) * 32);
             float* ml = mine + 16 * 32;
             float a1[NT][2], a2[NT][2];
 #pragma unroll
@@ -455,8 +537,8 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
 #pragma unroll
                             for (int x = 0; x < 2; ++x) {
                                 const float m2 = ml[(4 * k + x) * 32 + lane], l2 = ml[(4 * k + 2 + x) * 32 + lane];
-                                const float mn = fmaxf(m_run[k][x], m2), bs = mn == -INFINITY ? 0.f : mn;
-                                a1[k][x] = exp2f(m_run[k][x] - bs), a2[k][x] = exp2f(m2 - bs);
+                                const float mn = fmaxf(m_run[k][x], m2);
+                                a1[k][x] = exp2f(m_run[k][x] - mn), a2[k][x] = exp2f(m2 - mn);
                                 l_run[k][x] = l_run[k][x] * a1[k][x] + l2 * a2[k][x];
                                 m_run[k][x] = mn;
                             }
@@ -536,12 +618,11 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
             const long long c = c0 + p;
             return P.part + ((2 * c + (start <= c * chunk ? 0 : 1)) * P.Hq + h) * kPagedPartStride;
         };
-        float mx = -INFINITY;
+        float mx = kPagedNone;
         if (any)
             for (int p = lane; p < parts; p += 32) mx = fmaxf(mx, at(p)[kKvD]);
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-        const float bs = mx == -INFINITY ? 0.f : mx;
         float l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (any) {
@@ -550,7 +631,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
                 const float* src = at(p);
                 const float2 ml = *reinterpret_cast<const float2*>(src + kKvD);
                 const float4 v = *reinterpret_cast<const float4*>(src + lane * 4);
-                const float w = exp2f(ml.x - bs);
+                const float w = exp2f(ml.x - mx);
                 l += ml.y * w;
                 acc.x += v.x * w, acc.y += v.y * w, acc.z += v.z * w, acc.w += v.w * w;
             }

@@ -484,11 +484,13 @@ dsa_status run_rope(const void* x, int dtype, int64_t T, int H, int D, RopeParam
     P.rot_units = P.n / V;
     P.copy_vecs = in_place ? 0 : (D - 2 * P.n) / V;
     P.units = P.rot_units + (P.copy_vecs + 1) / 2;
-    // a block: whole tokens where they fit, as many heads of one otherwise
-    P.head_slots = std::min(H, std::max(1, kRopeThreads / P.units));
-    P.tokens = std::max(1, kRopeThreads / (P.units * P.head_slots));
     const int sms = num_sms();
     if (sms <= 0) return DSA_ERR_CUDA;
+    // heads of a thread: one while the call cannot fill the GPU's threads, then as many as fill them
+    const int64_t full = 512ll * sms;
+    const int per = (int)std::max<int64_t>(1, std::min<int64_t>(kRopeMostHeads, T * H * P.units / full));
+    P.head_slots = std::min((H + per - 1) / per, std::max(1, kRopeThreads / P.units));
+    P.tokens = std::max(1, kRopeThreads / (P.units * P.head_slots));
     const int64_t blocks = (T + P.tokens - 1) / P.tokens;
     const int grid = (int)std::min<int64_t>(blocks, 8ll * sms);
     LaunchScope ls(K_ROPE, s);

@@ -18,7 +18,8 @@
 namespace dsa {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeHeadsPerThread = 4;
+constexpr int kRopeBatch = 4;      // heads whose loads a thread has in flight together
+constexpr int kRopeMostHeads = 8;  // heads that share a thread's sines, where there are many tokens
 
 struct RopeParams {
     const void* x;
@@ -99,7 +100,7 @@ struct RopeElem<float> {
 // layout a holds the first members of V pairs and b the second; interleaved, a and b are adjacent and
 // hold V / 2 pairs each.  Copied units: two of the vectors outside [off, off + 2n), bits as they are.
 template <typename T, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) {
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_kernel(const RopeParams P) {
     using E = RopeElem<T>;
     constexpr int V = E::V;
     const int per_token = P.units * P.head_slots;
@@ -125,31 +126,36 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams P) 
     }
     const T* x = static_cast<const T*>(P.x);
     T* out = static_cast<T*>(P.out);
-    for (long long t = (long long)blockIdx.x * P.tokens + tl; t < P.T; t += (long long)gridDim.x * P.tokens) {
-        float c[V], s[V];
-        if (turned) {
-            const unsigned long long p =
-                static_cast<unsigned long long>(P.pos ? static_cast<long long>(P.pos[t]) : P.pos0 + t);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                E::sincos(static_cast<uint32_t>((p * f[i]) >> 32), c[i], s[i]);
-                c[i] *= P.mscale;
-                s[i] *= P.inverse ? -P.mscale : P.mscale;
-            }
-        }
+    const long long t0 = (long long)blockIdx.x * P.tokens + tl, dt = (long long)gridDim.x * P.tokens;
+    long long pos = t0 < P.T ? (P.pos ? (long long)P.pos[t0] : P.pos0 + t0) : 0;
+    for (long long t = t0; t < P.T; t += dt) {
         const T* xt = x + t * P.x_ts;
         T* ot = out + t * P.out_ts;
-        for (int hb = h0; hb < P.H; hb += P.head_slots * kRopeHeadsPerThread) {
-            uint4 va[kRopeHeadsPerThread], vb[kRopeHeadsPerThread];
+        uint4 va[kRopeBatch], vb[kRopeBatch];
+        auto load = [&](int hb) {
 #pragma unroll
-            for (int i = 0; i < kRopeHeadsPerThread; ++i) {
+            for (int i = 0; i < kRopeBatch; ++i) {
                 const int h = hb + i * P.head_slots;
                 if (h >= P.H) break;
                 va[i] = *reinterpret_cast<const uint4*>(xt + h * P.x_hs + a);
                 if (b >= 0) vb[i] = *reinterpret_cast<const uint4*>(xt + h * P.x_hs + b);
             }
+        };
+        load(h0);  // in flight while the sines are made
+        float c[V], s[V];
+        if (turned) {
 #pragma unroll
-            for (int i = 0; i < kRopeHeadsPerThread; ++i) {
+            for (int i = 0; i < V; ++i) {
+                E::sincos(static_cast<uint32_t>((static_cast<unsigned long long>(pos) * f[i]) >> 32), c[i], s[i]);
+                c[i] *= P.mscale;
+                s[i] *= P.inverse ? -P.mscale : P.mscale;
+            }
+        }
+        if (t + dt < P.T) pos = P.pos ? (long long)P.pos[t + dt] : P.pos0 + t + dt;
+        for (int hb = h0; hb < P.H; hb += P.head_slots * kRopeBatch) {
+            if (hb != h0) load(hb);
+#pragma unroll
+            for (int i = 0; i < kRopeBatch; ++i) {
                 const int h = hb + i * P.head_slots;
                 if (h >= P.H) break;
                 if (turned) {

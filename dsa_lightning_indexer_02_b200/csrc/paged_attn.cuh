@@ -17,9 +17,10 @@
 //   - V's scale 2^e * m, 1 <= m < 2, enters through the exponent: the softmax's reference is the running
 //     maximum of z + e, so that P = 2^(z + e - max) * m, rounded to fp16, keeps its bits however far the
 //     scales of a row's pages lie apart; the row sum adds P's 2^-e part in fp32.
-//   - Rows are dealt to blocks by tiles: block c of C takes tiles [c, c + 1) * ceil(W / C) of all rows' W, in
-//     order, whatever the rows' lengths.  A row that one block holds whole is finished there; of the
-//     others each block writes its unnormalised part, and paged_combine_kernel joins them.
+//   - Rows are dealt to blocks by units, a row's units being its tiles and one more for its end: block c of
+//     C takes units [c, c + 1) * ceil(U / C) of all rows' U, in order, whatever the rows' lengths.  A row that
+//     one block holds whole is finished there; of the others each block writes its unnormalised part, and
+//     paged_combine_kernel joins them.
 #pragma once
 
 #include "kv8.cuh"
@@ -29,7 +30,7 @@ namespace dsa {
 constexpr int kPagedPartCtas = 296;     // most blocks that share rows; each has two partial slots
 constexpr int kPagedSharedRows = 1184;  // with more rows, every row gets a block of its own
 constexpr int kPagedPartStride = kKvD + 4;  // floats of a partial: O[128], max, sum, 2 pad
-constexpr int kPagedMinTiles = 2;       // fewest tiles worth a block of their own
+constexpr int kPagedRowTiles = 1;       // what the end of a row costs a block, in tiles, when rows are dealt
 
 struct PagedParams {
     const __nv_bfloat16* q;            // [T, Hq, 128]
@@ -45,7 +46,7 @@ struct PagedParams {
     float* lse;                        // [T, Hq], may be null
     int shared_rows;                   // rows are dealt by tiles (and joined); otherwise one block each
     float* part;                       // [2 * gridDim.x, Hq, kPagedPartStride]
-    long long* row_start;              // [T + 1]: the rows' first tiles, and the tiles of a block behind them
+    long long* row_start;              // [T + 1]: where the rows start, in units dealt; behind them a block's units
 };
 
 // NT: groups of 8 query heads of a KV head.  KT: 16-key tiles of a warp's step.
@@ -60,7 +61,8 @@ struct PagedCfg {
     static constexpr int META = 68;                   // floats of a stage: K's and V's scales, mask
     static constexpr int RING_BYTES = NW * S * STAGE;
     static constexpr int META_BYTES = NW * S * META * 4;
-    static constexpr int XCH_BYTES = (NW / 2) * (16 + 4 * NT) * 32 * 4;
+    static constexpr int XCH_BYTES = NW * NT * 16 * 4;  // maxima and sums of a warp's heads
+    static_assert(NT * 8 * 4 * 32 * 4 <= STAGE, "a warp's outputs are exchanged through one of its stages");
     static constexpr int SMEM = RING_BYTES + META_BYTES + XCH_BYTES;
 };
 constexpr float kPagedNone = -1e30f;  // the running maximum before any key
@@ -92,18 +94,21 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Two stored bytes (of the low or the high half of w) as fp16 values.
-template <int FMT, bool HI>
-__device__ __forceinline__ uint32_t kv_f16x2(uint32_t w) {
+// Four stored bytes as fp16 values, two to a register.
+template <int FMT>
+__device__ __forceinline__ void kv_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if constexpr (FMT == KV_E4M3) {
-        uint32_t r;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(HI ? w >> 16 : w)));
-        return r;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
     } else {
         // byte + 128 in the low bits of the fp16 number 1024 is 1152 + byte
-        const uint32_t m = __byte_perm(w ^ 0x80808080u, 0x64646464u, HI ? 0x4342 : 0x4140);
-        const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&m), __half2half2(__ushort_as_half(0x6480)));
-        return *reinterpret_cast<const uint32_t*>(&r);
+        const uint32_t u = w ^ 0x80808080u, m0 = __byte_perm(u, 0x64646464u, 0x4140), m1 = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 c = __half2half2(__ushort_as_half(0x6480));
+        const __half2 r0 = __hsub2(*reinterpret_cast<const __half2*>(&m0), c);
+        const __half2 r1 = __hsub2(*reinterpret_cast<const __half2*>(&m1), c);
+        lo = *reinterpret_cast<const uint32_t*>(&r0), hi = *reinterpret_cast<const uint32_t*>(&r1);
     }
 }
 
@@ -121,20 +126,47 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     const int head = warp % HKV, sub = warp / HKV;
     const int g = lane >> 2, j = lane & 3;
 
-    // ---- this block's tiles [w0, w1), from tile `tile0` of row `row0` on
-    long long w0 = 0, w1;
+    // ---- this block's units [w0, w1); its first tile is `tile0` of row `row0`, which is unit `at`
+    long long w0 = 0, w1, at = 0;
     int row0 = blockIdx.x, tile0 = 0;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (P.shared_rows) {
-        __shared__ long long s_sum[NW], s_total;
-        __shared__ int s_row0, s_tile0;
+    auto row_tiles = [&](int r) {
+        int b, n;
+        paged_row(P, r, b, n);
+        return (paged_count(P, n) + TK - 1) / TK;
+    };
+    if (P.shared_rows && P.T <= 32) {
+        // every warp for itself, a row to a lane
+        const int nt = lane < P.T ? row_tiles(lane) : 0, mine = nt ? nt + kPagedRowTiles : 0;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const int total = __shfl_sync(0xffffffffu, incl, 31), chunk = max(1, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+        const int start = incl - mine;
+        w0 = (long long)blockIdx.x * chunk;
+        w1 = min((long long)total, w0 + chunk);
+        if (blockIdx.x == 0 && warp == 0) {
+            if (lane < P.T) P.row_start[lane] = start;
+            if (lane == 0) P.row_start[P.T] = chunk;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, nt && w0 < start + nt && start < w1);
+        if (!hit) return;
+        row0 = __ffs(hit) - 1;
+        const int s0 = __shfl_sync(0xffffffffu, start, row0);
+        tile0 = (int)max(0ll, w0 - s0);
+        at = s0 + tile0;
+    } else if (P.shared_rows) {
+        __shared__ long long s_sum[NW], s_total, s_start;
+        __shared__ int s_row0;
         const int per = (P.T + C::THREADS - 1) / C::THREADS;
         const int r0 = min(P.T, (int)threadIdx.x * per), r1 = min(P.T, r0 + per);
         long long mine = 0;
         for (int r = r0; r < r1; ++r) {
-            int b, n;
-            paged_row(P, r, b, n);
-            mine += (paged_count(P, n) + TK - 1) / TK;
+            const int nt = row_tiles(r);
+            mine += nt ? nt + kPagedRowTiles : 0;
         }
         long long incl = mine;
 #pragma unroll
@@ -152,31 +184,34 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                 run += x;
             }
             s_total = run;
+            s_row0 = P.T;
         }
         __syncthreads();
         const long long total = s_total;
-        const long long chunk = max((long long)kPagedMinTiles, (total + gridDim.x - 1) / gridDim.x);
+        const long long chunk = max(1ll, (total + gridDim.x - 1) / gridDim.x);
         w0 = blockIdx.x * chunk;
         w1 = min(total, w0 + chunk);
-        long long start = s_sum[warp] + incl - mine;
-        if (blockIdx.x == 0 || (w0 >= start && w0 < start + mine)) {
+        long long start = s_sum[warp] + incl - mine, found_start = 0;
+        int found = P.T;
+        if (blockIdx.x == 0 || (start < w1 && w0 < start + mine)) {
             for (int r = r0; r < r1; ++r) {
-                int b, n;
-                paged_row(P, r, b, n);
-                const int nt = (paged_count(P, n) + TK - 1) / TK;
-                if (w0 >= start && w0 < start + nt) s_row0 = r, s_tile0 = (int)(w0 - start);
+                const int nt = row_tiles(r);
+                if (found == P.T && nt && w0 < start + nt && start < w1) found = r, found_start = start;
                 if (blockIdx.x == 0) P.row_start[r] = start;
-                start += nt;
+                start += nt ? nt + kPagedRowTiles : 0;
             }
+            if (found < P.T) atomicMin(&s_row0, found);
         }
         if (blockIdx.x == 0 && threadIdx.x == 0) P.row_start[P.T] = chunk;
         __syncthreads();
-        if (w0 >= w1) return;
-        row0 = s_row0, tile0 = s_tile0;
+        row0 = s_row0;
+        if (row0 == P.T) return;
+        if (found == row0) s_start = found_start;
+        __syncthreads();
+        tile0 = (int)max(0ll, w0 - s_start);
+        at = s_start + tile0;
     } else {
-        int b, n;
-        paged_row(P, row0, b, n);
-        w1 = (paged_count(P, n) + TK - 1) / TK;
+        w1 = row_tiles(row0);
         if (w1 == 0) {  // a row without keys
             uint4* o = reinterpret_cast<uint4*>(P.out + (long long)row0 * P.Hq * kKvD);
             for (int i = threadIdx.x; i < P.Hq * kKvD / 8; i += C::THREADS) o[i] = make_uint4(0, 0, 0, 0);
@@ -185,7 +220,6 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
             return;
         }
     }
-    const int tiles = (int)(w1 - w0);
 
     uint8_t* ring = smem + warp * (S * C::STAGE);
     float* meta = reinterpret_cast<float*>(smem + C::RING_BYTES) + warp * (S * C::META);
@@ -194,28 +228,30 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     // ---- copies.  A step's keys pass three stages, one iteration apart: their numbers are loaded, their
     // pages looked up, their rows copied.  With IDX lane i has key i of the step (KT = 1: i mod 16);
     // otherwise lane i has the first key of 16-key tile i mod 16, for i mod 16 < KT.
-    int f_row = row0, f_tile = tile0, f_nt = 0, f_b = 0, f_n = 0, f_left = tiles;  // front cursor
-    if (tiles > 0) {
-        paged_row(P, f_row, f_b, f_n);
-        f_nt = (paged_count(P, f_n) + TK - 1) / TK;
-    }
+    int f_row = row0, f_tile = tile0, f_b, f_n;  // front cursor: the next tile whose keys are loaded
+    long long f_at = at;
+    paged_row(P, f_row, f_b, f_n);
+    int f_nt = (paged_count(P, f_n) + TK - 1) / TK;
     const int my_key = IDX ? (KT == 2 ? lane : lane & 15) : (lane & 15) * 16;
     const bool has_key = IDX || (lane & 15) < KT;
     int a_key = -1, a_n = 0, a_b = 0;  // numbers loaded
     int b_slot = -1, b_valid = 0;      // pages looked up: token's slot in the pool, -1 none; keys from it on
     auto load_keys = [&]() {
         a_key = -1;
-        if (f_left <= 0) return;
-        --f_left;
+        if (f_at >= w1) return;
         const int e = f_tile * TK + sub * (KT * 16) + my_key;
         a_n = f_n, a_b = f_b;
         if (has_key && e < paged_count(P, f_n)) a_key = IDX ? P.idx[(long long)f_row * P.topk + e] : e;
-        if (++f_tile == f_nt && f_left > 0) {
-            do {
-                paged_row(P, ++f_row, f_b, f_n);
-                f_nt = (paged_count(P, f_n) + TK - 1) / TK;
-            } while (f_nt == 0);
+        ++f_at;
+        if (++f_tile == f_nt) {
+            f_at += kPagedRowTiles;
             f_tile = 0;
+            if (f_at < w1) {  // some later row has units before w1
+                do {
+                    paged_row(P, ++f_row, f_b, f_n);
+                    f_nt = (paged_count(P, f_n) + TK - 1) / TK;
+                } while (f_nt == 0);
+            }
         }
     };
     auto look_up = [&]() {
@@ -299,14 +335,14 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     float o[NT][8][4], m_run[NT][2], l_run[NT][2];
     int row = row0, left;  // left: tiles of the row still to come in this block
     bool whole;            // the block holds the row from its first tile to its last
-    long long at = w0;     // flat number of the next tile
-    bool first_part = true;
+    int slot;              // where its part goes if not: 0 where the row reaches back to the block's first unit
     auto begin_row = [&](int tile) {
         int b, n;
         paged_row(P, row, b, n);
         const int nt = (paged_count(P, n) + TK - 1) / TK;
         left = (int)min((long long)(nt - tile), w1 - at);
         whole = tile == 0 && left == nt;
+        slot = at - tile <= w0 ? 0 : 1;
 #pragma unroll
         for (int nt8 = 0; nt8 < NT; ++nt8) {
             const int hl = nt8 * 8 + g;
@@ -345,7 +381,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     };
     begin_row(tile0);
 
-    for (int i = 0, st = 0; i < tiles; ++i) {
+    for (int st = 0;;) {
         cp_async_wait<S - 2>();
         __syncwarp();
         copy_rows(st == 0 ? S - 1 : st - 1);  // the stage that the last iteration used up
@@ -379,8 +415,9 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                     const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
-                        const uint32_t a[4] = {kv_f16x2<FMT, false>(xw[w]), kv_f16x2<FMT, false>(yw[w]),
-                                               kv_f16x2<FMT, true>(xw[w]), kv_f16x2<FMT, true>(yw[w])};
+                        uint32_t a[4];
+                        kv_f16x4<FMT>(xw[w], a[0], a[2]);
+                        kv_f16x4<FMT>(yw[w], a[1], a[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             mma_16816_f16(z[t][nt], a, qf[nt][half * 4 + w][0], qf[nt][half * 4 + w][1]);
@@ -482,112 +519,83 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                     for (int half = 0; half < 2; ++half) {
                         const uint32_t x = __byte_perm(aw[w], bw[w], half ? 0x7362 : 0x5140);
                         const uint32_t y = __byte_perm(ew[w], fw[w], half ? 0x7362 : 0x5140);
-                        const uint32_t a[4] = {kv_f16x2<FMT, false>(x), kv_f16x2<FMT, true>(x), kv_f16x2<FMT, false>(y),
-                                               kv_f16x2<FMT, true>(y)};
+                        uint32_t a[4];
+                        kv_f16x4<FMT>(x, a[0], a[1]);
+                        kv_f16x4<FMT>(y, a[2], a[3]);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) mma_16816_f16(o[nt][2 * w + half], a, pb[t][nt][0], pb[t][nt][1]);
                     }
                 }
             }
         }
+        const int used = st;
         st = st + 1 == S ? 0 : st + 1;
         ++at;
         if (--left) continue;
 
-        // ---- the row's last tile in this block: join the warps of a KV head, write
+        // ---- the row's last tile in this block: the warps of a KV head exchange their outputs through the
+        // stages that they have just used up, and each joins and writes every NSUB-th fragment
+        float* frag = reinterpret_cast<float*>(ring + used * C::STAGE) + lane;
+        float* ml = xch + warp * (NT * 16);  // [nt][maximum, sum][j][column]
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 float l = l_run[nt][x];
                 l += __shfl_xor_sync(0xffffffffu, l, 4);
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
-                l_run[nt][x] = l;
+                if (g == 0) ml[nt * 16 + j * 2 + x] = m_run[nt][x], ml[nt * 16 + 8 + j * 2 + x] = l;
             }
-        for (int n = NSUB; n > 1;) {
-            const int h = (n + 1) / 2;
-            const bool gives = sub >= h && sub < n, takes = sub < n - h;
-            float* mine = xch + (gives ? (sub - h) * HKV + head : sub * HKV + head) * ((16 + 4 * NT) * 32);
-            float* ml = mine + 16 * 32;
-            float a1[NT][2], a2[NT][2];
 #pragma unroll
-            for (int ph = 0; ph < 2 * NT; ++ph) {
-                constexpr int kHalf = 4;
-                const int nt = ph >> 1, dt0 = (ph & 1) * kHalf;
-                __syncthreads();  // the area is free
-                if (gives) {
-                    if (ph == 0) {
+            for (int dt = 0; dt < 8; ++dt)
 #pragma unroll
-                        for (int k = 0; k < NT; ++k) {
-                            ml[(4 * k) * 32 + lane] = m_run[k][0], ml[(4 * k + 1) * 32 + lane] = m_run[k][1];
-                            ml[(4 * k + 2) * 32 + lane] = l_run[k][0], ml[(4 * k + 3) * 32 + lane] = l_run[k][1];
-                        }
-                    }
+                for (int x = 0; x < 4; ++x) frag[((nt * 8 + dt) * 4 + x) * 32] = o[nt][dt][x];
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int i = sub; i < NT * 8; i += NSUB) {
+            const int nt = i >> 3, dt = i & 7;
+            const float2* mlh = reinterpret_cast<const float2*>(xch + head * (NT * 16) + nt * 16) + j;
+            float2 m = make_float2(kPagedNone, kPagedNone), l = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int dt = 0; dt < kHalf; ++dt)
+            for (int w = 0; w < NSUB; ++w) {
+                const float2 t = mlh[w * HKV * (NT * 8)];
+                m.x = fmaxf(m.x, t.x), m.y = fmaxf(m.y, t.y);
+            }
+            float a[4] = {0.f, 0.f, 0.f, 0.f};
+            const float* src = reinterpret_cast<const float*>(smem + head * (S * C::STAGE) + used * C::STAGE) + (nt * 8 + dt) * 128 + lane;
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) mine[(dt * 4 + x) * 32 + lane] = o[nt][dt0 + dt][x];
-                }
-                __syncthreads();
-                if (takes) {
-                    if (ph == 0) {
+            for (int w = 0; w < NSUB; ++w) {
+                const float2 t = mlh[w * HKV * (NT * 8)], u = mlh[w * HKV * (NT * 8) + 4];
+                const float wx = exp2f(t.x - m.x), wy = exp2f(t.y - m.y);
+                l.x += u.x * wx, l.y += u.y * wy;
+                const float* p = src + w * HKV * (S * C::STAGE / 4);
+                a[0] += p[0] * wx, a[1] += p[32] * wy, a[2] += p[64] * wx, a[3] += p[96] * wy;
+            }
 #pragma unroll
-                        for (int k = 0; k < NT; ++k)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float m2 = ml[(4 * k + x) * 32 + lane], l2 = ml[(4 * k + 2 + x) * 32 + lane];
-                                const float mn = fmaxf(m_run[k][x], m2);
-                                a1[k][x] = exp2f(m_run[k][x] - mn), a2[k][x] = exp2f(m2 - mn);
-                                l_run[k][x] = l_run[k][x] * a1[k][x] + l2 * a2[k][x];
-                                m_run[k][x] = mn;
-                            }
-                    }
-#pragma unroll
-                    for (int dt = 0; dt < kHalf; ++dt)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            o[nt][dt0 + dt][x] = o[nt][dt0 + dt][x] * a1[nt][x & 1] + mine[(dt * 4 + x) * 32 + lane] * a2[nt][x & 1];
+            for (int x = 0; x < 2; ++x) {
+                const int hl = nt * 8 + 2 * j + x;
+                if (hl >= G) continue;
+                const long long h = (long long)row * P.Hq + head * G + hl;
+                const float mx = x ? m.y : m.x, lx = x ? l.y : l.x;
+                if (whole) {
+                    const float inv = lx == 0.f ? 0.f : 1.f / lx;
+                    *reinterpret_cast<uint32_t*>(P.out + h * kKvD + 16 * g + 2 * dt) = pack_bf16x2(a[x] * inv, a[2 + x] * inv);
+                    if (P.lse && g == 0 && dt == 0) P.lse[h] = lx == 0.f ? -INFINITY : (mx + log2f(lx)) * 0.69314718055994531f;
+                } else {
+                    float* part = P.part + ((2ll * blockIdx.x + slot) * P.Hq + head * G + hl) * kPagedPartStride;
+                    *reinterpret_cast<float2*>(part + 16 * g + 2 * dt) = make_float2(a[x], a[2 + x]);
+                    if (g == 0 && dt == 0) *reinterpret_cast<float2*>(part + kKvD) = make_float2(mx, lx);
                 }
             }
-            n = h;
         }
-        if (sub == 0) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int hl = nt * 8 + 2 * j + x;
-                    if (hl >= G) continue;
-                    const int h = head * G + hl;
-                    if (whole) {
-                        const float inv = l_run[nt][x] == 0.f ? 0.f : 1.f / l_run[nt][x];
-                        uint32_t w[8];
-#pragma unroll
-                        for (int dt = 0; dt < 8; ++dt) w[dt] = pack_bf16x2(o[nt][dt][x] * inv, o[nt][dt][2 + x] * inv);
-                        uint4* dst = reinterpret_cast<uint4*>(P.out + ((long long)row * P.Hq + h) * kKvD + 16 * g);
-                        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                        if (P.lse && g == 0)
-                            P.lse[(long long)row * P.Hq + h] =
-                                l_run[nt][x] == 0.f ? -INFINITY : (m_run[nt][x] + log2f(l_run[nt][x])) * 0.69314718055994531f;
-                    } else {
-                        float* part = P.part + ((2ll * blockIdx.x + (first_part ? 0 : 1)) * P.Hq + h) * kPagedPartStride;
-                        float4* dst = reinterpret_cast<float4*>(part + 16 * g);
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-                            dst[w] = make_float4(o[nt][2 * w][x], o[nt][2 * w][2 + x], o[nt][2 * w + 1][x], o[nt][2 * w + 1][2 + x]);
-                        if (g == 0) part[kKvD] = m_run[nt][x], part[kKvD + 1] = l_run[nt][x];
-                    }
-                }
-        }
-        first_part = false;
-        if (i + 1 < tiles) {
-            int b, n;
-            do paged_row(P, ++row, b, n);
-            while (paged_count(P, n) == 0);
-            begin_row(0);
-        }
+        at += kPagedRowTiles;
+        if (at >= w1) break;
+        do ++row;
+        while (row_tiles(row) == 0);
+        begin_row(0);
+        __syncthreads();  // the stages are read: the next copies may take them
     }
 }
 

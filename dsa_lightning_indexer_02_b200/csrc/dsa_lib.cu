@@ -508,16 +508,17 @@ dsa_status run_rope(const void* x, int dtype, int64_t T, int H, int D, RopeParam
 bool page_supported(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 int log2_of(int x) { return 31 - __builtin_clz((unsigned)x); }
 
-template <int FMT>
-dsa_status launch_append_t(const AppendParams& P, int64_t units, cudaStream_t s) {
-    auto kern = kv_append_kernel<FMT>;
+template <int FMT, bool INTER>
+dsa_status launch_append_t(AppendParams P, int64_t units, cudaStream_t s) {
+    auto kern = kv_append_kernel<FMT, INTER>;
     static DeviceFlags attr_set;
     if (!set_smem_limit(kern, 128 * (kKvD / 2) * 8, attr_set)) return DSA_ERR_CUDA;
-    const int page = 1 << P.page_shift;
-    const int tokens = P.cu_new ? page : 1;  // most tokens of a block
-    const int threads = std::min(512, std::max(128, tokens * P.Hkv * kKvUnits / kAppendPasses));
+    const int tokens = P.cu_new ? 1 << P.page_shift : 1;  // most tokens of a block
+    const int heads = std::min(P.Hkv, kAppendRows / tokens);
+    P.hg_shift = log2_of(heads);
+    const int threads = std::max(64, tokens * heads * kKvUnits / kAppendPasses);
     LaunchScope ls(K_KV_APPEND, s);
-    kern<<<dim3((unsigned)units, 2), threads, tokens * P.n * 8, s>>>(P);
+    kern<<<dim3((unsigned)units, 2 * P.Hkv / heads), threads, tokens * P.n * 8, s>>>(P);
     return launch_status();
 }
 
@@ -1137,10 +1138,13 @@ dsa_status dsa_kv_append(const void* k_new, const void* v_new, int64_t k_ts, int
     P.table = page_table, P.ctx_len = ctx_len, P.cu_new = cu_new, P.rope_pos = rope_pos, P.inv_freq = inv_freq;
     P.B = B, P.N = (int)N, P.Hkv = Hkv, P.page_shift = log2_of(page_size), P.max_pages = max_pages;
     P.num_pages = num_pages;
-    P.n = rot_dim / 2, P.off = rot_offset, P.inter = layout == DSA_ROPE_INTERLEAVED, P.mscale = mscale;
+    P.n = rot_dim / 2, P.off = rot_dim ? rot_offset : 0, P.mscale = mscale;
+    const bool inter = rot_dim && layout == DSA_ROPE_INTERLEAVED;
     const int64_t units = cu_new ? (N >> P.page_shift) + 2 * (int64_t)B : B;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return kv_format == DSA_KV_E4M3 ? launch_append_t<KV_E4M3>(P, units, s) : launch_append_t<KV_INT8>(P, units, s);
+    if (kv_format == DSA_KV_E4M3)
+        return inter ? launch_append_t<KV_E4M3, true>(P, units, s) : launch_append_t<KV_E4M3, false>(P, units, s);
+    return inter ? launch_append_t<KV_INT8, true>(P, units, s) : launch_append_t<KV_INT8, false>(P, units, s);
 }
 
 dsa_status dsa_paged_attn(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,

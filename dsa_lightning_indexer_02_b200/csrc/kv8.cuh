@@ -9,10 +9,14 @@
 // (down to its subnormals), cost e4m3 no precision, and make every stored value exact in bf16 and,
 // unscaled, in fp16.
 //
-// Append: one block per touched page for K and one for V; the page's new rows stay in registers
-// (packed bf16) between the pass that finds each head's largest magnitude and the pass that rounds,
-// so every input is read once and every byte written once.  The block's sines and cosines are made
-// once per (token, pair) in shared memory and serve all its KV heads.
+// Append: one block per touched page (of up to 256 rows of a token and head) for K and one for V.  A thread
+// owns 16 dims of four rows at most, both members of the pairs that it turns; they stay in registers
+// between finding each head's largest magnitude and rounding, so every input is read once and every byte
+// written once.  The sines and cosines are made once per (token, pair) in shared memory for all heads.
+//
+// Rounding of turned keys: fp32's own error moves one value in some 10^5 across a border between two 8-bit
+// values.  Where the interval of twice that error around a value rounds to two different bytes, the pair is
+// computed again in fp64, so the stored byte is the exact product's.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -24,8 +28,9 @@ namespace dsa {
 
 constexpr int kKvD = 128;
 constexpr int kKvEMin = -64;       // least scale exponent (an all-zero block gets it)
-constexpr int kKvUnits = 16;       // 8-dim units of a token and head
-constexpr int kAppendPasses = 16;  // units per thread of the append kernel
+constexpr int kKvUnits = 8;        // 16-dim units of a row (a token and head)
+constexpr int kAppendPasses = 4;   // most units of a thread
+constexpr int kAppendRows = 256;   // most rows of a block
 
 enum { KV_E4M3 = 0, KV_INT8 = 1 };
 
@@ -40,7 +45,7 @@ struct AppendParams {
     const int* rope_pos;                 // [N], or null: the cache position
     const double* inv_freq;              // [n], null when n == 0
     int B, N, Hkv, page_shift, max_pages, num_pages;
-    int n, off, inter;
+    int n, off, hg_shift;  // hg_shift: log2 of the heads of a block
     float mscale;
 };
 
@@ -133,148 +138,223 @@ __device__ __forceinline__ AppendSpan append_span(const AppendParams& P, int uni
     return S;
 }
 
-template <int FMT>
+// Largest of 16 magnitudes; infinities and NaN do not count.
+__device__ __forceinline__ float kv_amax(const float (&f)[16]) {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(f[j]));  // passes NaN over
+    if (m == INFINITY) {
+        m = 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (fabsf(f[j]) < INFINITY) m = fmaxf(m, fabsf(f[j]));
+    }
+    return m;
+}
+
+// y to fp32 so that rounding the result again, to fewer bits, gives what rounding y itself gives: towards
+// zero, with the last bit set where anything was cut off.
+__device__ __forceinline__ float round_odd(double y) {
+    const float r = __double2float_rz(y);
+    return static_cast<double>(r) == y || !(y == y) ? r : __uint_as_float(__float_as_uint(r) | 1u);
+}
+
+template <int FMT, bool INTER>
 __global__ void __launch_bounds__(512) kv_append_kernel(const AppendParams P) {
-    extern __shared__ __align__(16) float2 s_turn[];  // [tokens][n]: cos, sin (K blocks)
+    extern __shared__ __align__(16) float2 s_turn[];  // [tokens][n]: cos, sin times mscale (K blocks)
     __shared__ unsigned s_amax[4];
     __shared__ float s_old[4], s_new[4];
-    const int lane = threadIdx.x & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const bool is_k = (blockIdx.y & 1) == 0;
+    const int n = is_k ? P.n : 0, hshift = P.hg_shift, hmask = (1 << hshift) - 1, h0 = (blockIdx.y >> 1) << hshift;
+    // the pair whose sines this thread makes, for every tstep-th token
+    const int pair = n ? tid % n : 0, tstep = n ? blockDim.x / n : 1, tfirst = n ? tid / n : 0;
+    const double freq = n ? P.inv_freq[pair] : 0.0;
+
     const AppendSpan S = append_span(P, blockIdx.x, lane);
     if (!S.any) return;
-    const bool is_k = blockIdx.y == 0;
-    const int Hkv = P.Hkv, page = 1 << P.page_shift;
-    const int pid = P.table[(long long)S.b * P.max_pages + S.pj];
-    if (pid < 0 || pid >= P.num_pages) {
-        if (threadIdx.x == 0) record_error(DSA_DEV_ERR_BOUNDS, 0xa03);
-        return;
-    }
-    uint8_t* pages = (is_k ? P.k_pages : P.v_pages) + (long long)pid * page * Hkv * kKvD;
-    float* scale = (is_k ? P.k_scale : P.v_scale) + (long long)pid * Hkv;
-    const __nv_bfloat16* x = is_k ? P.k_new : P.v_new;
-    const long long ts = is_k ? P.k_ts : P.v_ts, hs = is_k ? P.k_hs : P.v_hs;
-    const int tokens = S.i1 - S.i0, slot0 = S.p0 & (page - 1);
-    const int n = is_k ? P.n : 0;
-    if (threadIdx.x < Hkv) {
-        s_amax[threadIdx.x] = 0u;
-        s_old[threadIdx.x] = slot0 ? scale[threadIdx.x] : 0.f;
-    }
+    const int page = 1 << P.page_shift, tokens = S.i1 - S.i0, slot0 = S.p0 & (page - 1);
 
-    // unit i of this thread: row (token, head) of the page, dims 8 d8 .. 8 d8 + 7
-    const int d8 = threadIdx.x & (kKvUnits - 1);
-    const int row0 = threadIdx.x / kKvUnits, rows = tokens * Hkv, step = blockDim.x / kKvUnits;
-    uint4 raw[kAppendPasses];
+    // unit u of a row: two vectors of 8 dims, a and b.  Turned: in the half layout the first and the second
+    // members of 8 pairs, interleaved 4 adjacent pairs each; otherwise two of the vectors left over.
+    const int u = tid & (kKvUnits - 1), turned_units = n / 8;
+    const bool turned = u < turned_units;
+    int a, b;
+    if (turned) {
+        a = P.off + (INTER ? 16 * u : 8 * u);
+        b = INTER ? a + 8 : a + n;
+    } else {
+        const int v0 = u - turned_units, v1 = v0 + kKvUnits - turned_units, lead = is_k ? P.off / 8 : 0;
+        a = v0 < lead || !n ? v0 * 8 : v0 * 8 + 2 * n;
+        b = v1 < lead || !n ? v1 * 8 : v1 * 8 + 2 * n;
+    }
+    const int row0 = tid / kKvUnits, rows = tokens << hshift, step = blockDim.x / kKvUnits;  // step: whole tokens
+    const __nv_bfloat16* in = (is_k ? P.k_new : P.v_new) + (long long)S.i0 * (is_k ? P.k_ts : P.v_ts) +
+                             (long long)h0 * (is_k ? P.k_hs : P.v_hs);
+    const long long ts = is_k ? P.k_ts : P.v_ts, hs = is_k ? P.k_hs : P.v_hs;
+    const int my_h = row0 & hmask;  // the same for all rows of this thread
+    uint4 ra[kAppendPasses], rb[kAppendPasses];
 #pragma unroll
     for (int i = 0; i < kAppendPasses; ++i) {
         const int r = row0 + i * step;
-        if (r < rows)
-            raw[i] = *reinterpret_cast<const uint4*>(x + (long long)(S.i0 + r / Hkv) * ts + (r % Hkv) * hs + d8 * 8);
+        if (r < rows) {
+            const __nv_bfloat16* at = in + (long long)(r >> hshift) * ts + my_h * hs;
+            ra[i] = *reinterpret_cast<const uint4*>(at + a);
+            rb[i] = *reinterpret_cast<const uint4*>(at + b);
+        }
     }
-    if (n) {
-        for (int e = threadIdx.x; e < tokens * n; e += blockDim.x) {
-            const int t = e / n, p = e % n;
-            const long long pos = P.rope_pos ? P.rope_pos[S.i0 + t] : S.p0 + t;
+    const int pid = P.table[(long long)S.b * P.max_pages + S.pj];
+    if (pid < 0 || pid >= P.num_pages) {
+        if (tid == 0) record_error(DSA_DEV_ERR_BOUNDS, 0xa03);
+        return;
+    }
+    uint8_t* pages = (is_k ? P.k_pages : P.v_pages) + (long long)pid * page * P.Hkv * kKvD;
+    float* scale = (is_k ? P.k_scale : P.v_scale) + (long long)pid * P.Hkv + h0;
+    if (tid <= hmask) {
+        s_amax[tid] = 0u;
+        s_old[tid] = slot0 ? scale[tid] : 0.f;
+    }
+    const unsigned long long turn = rope_turn(freq);
+    auto position = [&](int t) {
+        return static_cast<unsigned long long>(P.rope_pos ? (long long)P.rope_pos[S.i0 + t] : (long long)(S.p0 + t));
+    };
+    if (n && tfirst < tstep) {
+        for (int t = tfirst; t < tokens; t += tstep) {
             float c, s;
-            rope_sincos((uint32_t)((static_cast<unsigned long long>(pos) * rope_turn(P.inv_freq[p])) >> 32), c, s);
-            s_turn[e] = make_float2(c * P.mscale, s * P.mscale);
+            rope_sincos(static_cast<uint32_t>((position(t) * turn) >> 32), c, s);
+            s_turn[t * n + pair] = make_float2(c * P.mscale, s * P.mscale);
         }
     }
     __syncthreads();
 
-    // the row's 8 values in fp32, turned (all lanes of the warp take part)
-    const int a8 = P.off / 8, n8 = n / 8;
-    const bool turned = n && d8 >= a8 && d8 < a8 + 2 * n8;
-    const bool second = turned && !P.inter && d8 >= a8 + n8;
-    const int src = (lane & 16) | (turned && !P.inter ? (second ? d8 - n8 : d8 + n8) : d8);
-    auto values = [&](const uint4& v, int r, float (&f)[8]) {
-        RopeElem<__nv_bfloat16>::unpack(v, f);
-        if (!n) return;
-        if (P.inter) {
-            if (!turned) return;
-            const float2* cs = s_turn + (r / Hkv) * n + (d8 - a8) * 4;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 t = cs[j];
-                const float e0 = f[2 * j], e1 = f[2 * j + 1];
-                f[2 * j] = e0 * t.x - e1 * t.y;
-                f[2 * j + 1] = e0 * t.y + e1 * t.x;
-            }
-        } else {
-            uint4 w;
-            w.x = __shfl_sync(0xffffffffu, v.x, src), w.y = __shfl_sync(0xffffffffu, v.y, src);
-            w.z = __shfl_sync(0xffffffffu, v.z, src), w.w = __shfl_sync(0xffffffffu, v.w, src);
-            if (!turned) return;
-            float g[8];
-            RopeElem<__nv_bfloat16>::unpack(w, g);
-            const float2* cs = s_turn + (r / Hkv) * n + (second ? d8 - a8 - n8 : d8 - a8) * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 t = cs[j];
-                f[j] = second ? g[j] * t.y + f[j] * t.x : f[j] * t.x - g[j] * t.y;
-            }
-        }
-    };
-
-    // pass 1: the largest finite magnitude of each head
-    const int passes = (rows + step - 1) / step;  // uniform over the block
+    // values in fp32: f[0..8) of vector a, f[8..16) of vector b
+    float f[kAppendPasses][16];
+    float m = 0.f;
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < kAppendPasses; ++i) {
-        if (i >= passes) break;
         const int r = row0 + i * step;
-        const bool in = r < rows;
-        float f[8];
-        values(in ? raw[i] : make_uint4(0, 0, 0, 0), in ? r : 0, f);
-        float m = 0.f;
+        if (r >= rows) break;
+        float p[8], q[8];
+        RopeElem<__nv_bfloat16>::unpack(ra[i], p);
+        RopeElem<__nv_bfloat16>::unpack(rb[i], q);
+        if (turned) {
+            const float4* cs = reinterpret_cast<const float4*>(s_turn + (r >> hshift) * n + u * 8);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float v = fabsf(f[j]);
-            if (v < INFINITY) m = fmaxf(m, v);
-            nan |= in && !(f[j] == f[j]);
+            for (int j = 0; j < 8; j += 2) {
+                const float4 t = cs[j / 2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int x = j + k;
+                    const float c = k ? t.z : t.x, s = k ? t.w : t.y;
+                    const float e0 = INTER ? (x < 4 ? p[2 * x % 8] : q[2 * x % 8]) : p[x];
+                    const float e1 = INTER ? (x < 4 ? p[(2 * x + 1) % 8] : q[(2 * x + 1) % 8]) : q[x];
+                    const float y0 = e0 * c - e1 * s, y1 = e0 * s + e1 * c;
+                    f[i][INTER ? 2 * x : x] = y0, f[i][INTER ? 2 * x + 1 : 8 + x] = y1;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[i][j] = p[j], f[i][8 + j] = q[j];
         }
+        m = fmaxf(m, kv_amax(f[i]));
+        if (FMT == KV_INT8) {
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (in && d8 == 0) atomicMax(&s_amax[r % Hkv], __float_as_uint(m));  // m >= 0: bits keep the order
+            for (int j = 0; j < 16; ++j) nan |= !(f[i][j] == f[i][j]);
+        }
     }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (u == 0 && row0 < rows) atomicMax(&s_amax[my_h], __float_as_uint(m));  // m >= 0: bits keep the order
     if (FMT == KV_INT8 && nan) record_error(DSA_DEV_ERR_BOUNDS, 0xa04);
     __syncthreads();
-    if (threadIdx.x < Hkv) {
-        const float s = fmaxf(s_old[threadIdx.x], kv_pow2(kv_exponent<FMT>(__uint_as_float(s_amax[threadIdx.x]))));
-        s_new[threadIdx.x] = s;
-        scale[threadIdx.x] = s;
+    if (tid <= hmask) {
+        const float s = fmaxf(s_old[tid], kv_pow2(kv_exponent<FMT>(__uint_as_float(s_amax[tid]))));
+        s_new[tid] = s;
+        scale[tid] = s;
     }
     __syncthreads();
 
-    // pass 2: round and store the new rows
+    // round and store the new rows
+    const float s = s_new[my_h], inv = 1.f / s;  // powers of two
+    uint8_t* to = pages + (long long)slot0 * P.Hkv * kKvD + (h0 + my_h) * kKvD;
 #pragma unroll
     for (int i = 0; i < kAppendPasses; ++i) {
-        if (i >= passes) break;
         const int r = row0 + i * step;
-        const bool in = r < rows;
-        float f[8];
-        values(in ? raw[i] : make_uint4(0, 0, 0, 0), in ? r : 0, f);
-        if (!in) continue;
-        const float s = s_new[r % Hkv];
-        const float inv = 1.f / s;  // a power of two
-        uint2 w;
-        w.x = kv_round4<FMT>(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-        w.y = kv_round4<FMT>(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
-        *reinterpret_cast<uint2*>(pages + ((long long)slot0 * Hkv + r) * kKvD + d8 * 8) = w;
+        if (r >= rows) break;
+        uint32_t w[4];
+        if (!turned) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = kv_round4<FMT>(f[i][4 * k] * inv, f[i][4 * k + 1] * inv, f[i][4 * k + 2] * inv, f[i][4 * k + 3] * inv);
+        } else {
+            // pair x lies in bytes lo(x), hi(x); both ends of its error's interval are rounded.  The sine and
+            // cosine are off by 2^-23 of 1 at most (their own ulp, the angle's rounding, mscale's), products and
+            // sum by 2^-24, in all 2^-22.4 (|a| + |b|) <= 2^-21.9 (|y0| + |y1|).
+            float d[16];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int lo = INTER ? 2 * x : x, hi = INTER ? 2 * x + 1 : 8 + x;
+                d[lo] = d[hi] = (fabsf(f[i][lo]) + fabsf(f[i][hi])) * inv * 4.76837158203125e-7f;  // 2^-21
+            }
+            unsigned differ[4], any = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float v[4], x[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    v[y] = fmaf(f[i][4 * k + y], inv, -d[4 * k + y]);
+                    x[y] = fmaf(f[i][4 * k + y], inv, d[4 * k + y]);
+                }
+                w[k] = kv_round4<FMT>(v[0], v[1], v[2], v[3]);
+                differ[k] = w[k] ^ kv_round4<FMT>(x[0], x[1], x[2], x[3]);
+                any |= differ[k];
+            }
+            if (any) {
+                const __nv_bfloat16* at = in + (long long)(r >> hshift) * ts + my_h * hs;
+                const unsigned long long p = position(r >> hshift);
+#pragma unroll 1
+                for (int y = 0; y < 8; ++y) {
+                    const int lo = INTER ? 2 * y : y, hi = INTER ? 2 * y + 1 : 8 + y;
+                    const unsigned at_lo = 255u << (8 * (lo & 3)), at_hi = 255u << (8 * (hi & 3));
+                    unsigned dl = 0, dh = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) dl = lo >> 2 == k ? differ[k] : dl, dh = hi >> 2 == k ? differ[k] : dh;
+                    if (!((dl & at_lo) | (dh & at_hi))) continue;
+                    double sd, cd;
+                    const unsigned long long ph = p * rope_turn(P.inv_freq[u * 8 + y]);
+                    sincospi(static_cast<double>(static_cast<long long>(ph)) * 1.0842021724855044e-19, &sd, &cd);  // 2^-63
+                    const double e0 = __bfloat162float(at[lo < 8 ? a + lo : b + lo - 8]);
+                    const double e1 = __bfloat162float(at[hi < 8 ? a + hi : b + hi - 8]);
+                    const float y0 = round_odd(P.mscale * (e0 * cd - e1 * sd)), y1 = round_odd(P.mscale * (e0 * sd + e1 * cd));
+                    const uint32_t both = kv_round4<FMT>(y0 * inv, y1 * inv, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (lo >> 2 == k) w[k] = (w[k] & ~at_lo) | ((both & 255u) << (8 * (lo & 3)));
+                        if (hi >> 2 == k) w[k] = (w[k] & ~at_hi) | ((both >> 8 & 255u) << (8 * (hi & 3)));
+                    }
+                }
+            }
+        }
+        uint8_t* dst = to + (long long)(r >> hshift) * P.Hkv * kKvD;
+        *reinterpret_cast<uint2*>(dst + a) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(dst + b) = make_uint2(w[2], w[3]);
     }
 
     // tokens that the page held before: rounded again where their head's scale grew
     if (!slot0) return;
-    for (int e = threadIdx.x; e < slot0 * Hkv * 8; e += blockDim.x) {
-        const int h = (e >> 3) % Hkv;
+    for (int e = tid; e < slot0 << (hshift + 3); e += blockDim.x) {
+        const int h = (e >> 3) & hmask;
         if (s_old[h] == s_new[h]) continue;
         const float ratio = s_old[h] / s_new[h];
-        uint4* at = reinterpret_cast<uint4*>(pages + (long long)(e >> 3) * kKvD) + (e & 7);
+        uint4* at = reinterpret_cast<uint4*>(pages + ((long long)(e >> (hshift + 3)) * P.Hkv + h0 + h) * kKvD) + (e & 7);
         const uint4 v = *at;
         uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float f[4];
-            kv_value4<FMT>(w[i], f);
-            w[i] = kv_round4<FMT>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+            float x[4];
+            kv_value4<FMT>(w[i], x);
+            w[i] = kv_round4<FMT>(x[0] * ratio, x[1] * ratio, x[2] * ratio, x[3] * ratio);
         }
         *at = make_uint4(w[0], w[1], w[2], w[3]);
     }

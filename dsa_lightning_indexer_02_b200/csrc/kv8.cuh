@@ -9,7 +9,7 @@
 // (down to its subnormals), cost e4m3 no precision, and make every stored value exact in bf16 and,
 // unscaled, in fp16.
 //
-// Append: one block per touched page (of up to 256 rows of a token and head) for K and one for V.  A thread
+// Append: one block per touched page (of up to 128 rows of a token and head) for K and one for V.  A thread
 // owns 16 dims of four rows at most, both members of the pairs that it turns; they stay in registers
 // between finding each head's largest magnitude and rounding, so every input is read once and every byte
 // written once.  The sines and cosines are made once per (token, pair) in shared memory for all heads.
@@ -30,7 +30,7 @@ constexpr int kKvD = 128;
 constexpr int kKvEMin = -64;       // least scale exponent (an all-zero block gets it)
 constexpr int kKvUnits = 8;        // 16-dim units of a row (a token and head)
 constexpr int kAppendPasses = 4;   // most units of a thread
-constexpr int kAppendRows = 256;   // most rows of a block
+constexpr int kAppendRows = 128;   // most rows of a block
 
 enum { KV_E4M3 = 0, KV_INT8 = 1 };
 
@@ -66,9 +66,12 @@ __device__ __forceinline__ float kv_pow2(int e) { return __uint_as_float(static_
 template <int FMT>
 __device__ __forceinline__ uint32_t kv_round4(float a, float b, float c, float d) {
     if constexpr (FMT == KV_E4M3) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-        return lo | hi << 16;
+        uint32_t w;
+        asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
+            : "=r"(w)
+            : "f"(a), "f"(b), "f"(c), "f"(d));
+        return w;
     } else {
         auto r = [](float v) { return static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(v == v ? v : 0.f, -127.f), 127.f))) & 255u; };
         return r(a) | r(b) << 8 | r(c) << 16 | r(d) << 24;
@@ -97,13 +100,14 @@ struct AppendSpan {
 };
 __device__ __forceinline__ AppendSpan append_span(const AppendParams& P, int unit, int lane) {
     AppendSpan S{};
-    int i0, n, j;
+    int i0, n, j = 0, ctx;
     if (!P.cu_new) {
-        S.b = unit, i0 = unit, n = 1, j = 0;
+        S.b = unit, i0 = unit, n = 1, ctx = P.ctx_len[unit];
     } else {
-        // the last sequence whose first block is not behind this one, 32 candidates a step
+        // the last sequence whose first block is not behind this one: 32 candidates a step, the last step's
+        // with what the block needs to know of each
         int lo = 0, hi = P.B;  // the answer lies in [lo, hi)
-        while (hi - lo > 1) {
+        while (hi - lo > 32) {
             const int step = (hi - lo + 31) >> 5;
             const int b = lo + lane * step;
             const bool ok = b < hi && (P.cu_new[b] >> P.page_shift) + 2 * b <= unit;
@@ -112,18 +116,22 @@ __device__ __forceinline__ AppendSpan append_span(const AppendParams& P, int uni
             lo += last * step;
             hi = min(hi, lo + step);
         }
-        S.b = lo;
-        i0 = P.cu_new[lo];
-        const int i1 = P.cu_new[lo + 1];
+        const int b = min(lo + lane, hi - 1);
+        const int c0 = P.cu_new[b], c1 = P.cu_new[b + 1], cx = P.ctx_len[b];
+        const unsigned m = __ballot_sync(0xffffffffu, lo + lane < hi && (c0 >> P.page_shift) + 2 * b <= unit);
+        const int last = m ? 31 - __clz(m) : 0;
+        S.b = lo + last;
+        i0 = __shfl_sync(0xffffffffu, c0, last);
+        const int i1 = __shfl_sync(0xffffffffu, c1, last);
+        ctx = __shfl_sync(0xffffffffu, cx, last);
         if (i0 < 0 || i1 < i0 || i1 > P.N) {
             record_error(DSA_DEV_ERR_BOUNDS, 0xa01);
             return S;
         }
         n = i1 - i0;
-        j = unit - (i0 >> P.page_shift) - 2 * lo;
+        j = unit - (i0 >> P.page_shift) - 2 * S.b;
     }
     if (n <= 0 || j < 0) return S;
-    const int ctx = P.ctx_len[S.b];
     const long long cap = (long long)P.max_pages << P.page_shift;
     if (ctx < 0 || (long long)ctx + n > cap) {
         record_error(DSA_DEV_ERR_BOUNDS, 0xa02);
@@ -160,15 +168,18 @@ __device__ __forceinline__ float round_odd(double y) {
 }
 
 template <int FMT, bool INTER>
-__global__ void __launch_bounds__(512) kv_append_kernel(const AppendParams P) {
-    extern __shared__ __align__(16) float2 s_turn[];  // [tokens][n]: cos, sin times mscale (K blocks)
+__global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams P) {
+    // cos, sin times mscale (K blocks), [tokens][4][n / 8][2]: pairs 2 k, 2 k + 1 of unit u at [k][u], so that the
+    // units' 16-byte reads lie side by side
+    extern __shared__ __align__(16) float2 s_turn[];
     __shared__ unsigned s_amax[4];
     __shared__ float s_old[4], s_new[4];
     const int tid = threadIdx.x, lane = tid & 31;
     const bool is_k = (blockIdx.y & 1) == 0;
     const int n = is_k ? P.n : 0, hshift = P.hg_shift, hmask = (1 << hshift) - 1, h0 = (blockIdx.y >> 1) << hshift;
-    // the pair whose sines this thread makes, for every tstep-th token
-    const int pair = n ? tid % n : 0, tstep = n ? blockDim.x / n : 1, tfirst = n ? tid / n : 0;
+    // the pair whose sines this thread makes, for every tstep-th token, in the order of s_turn
+    const int entry = n ? tid % n : 0, tstep = n ? blockDim.x / n : 1, tfirst = n ? tid / n : 0;
+    const int pair = n ? (entry / 2 % (n / 8)) * 8 + entry / (n / 4) * 2 + (entry & 1) : 0;
     const double freq = n ? P.inv_freq[pair] : 0.0;
 
     const AppendSpan S = append_span(P, blockIdx.x, lane);
@@ -204,16 +215,6 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const AppendParams P) {
         }
     }
     const int pid = P.table[(long long)S.b * P.max_pages + S.pj];
-    if (pid < 0 || pid >= P.num_pages) {
-        if (tid == 0) record_error(DSA_DEV_ERR_BOUNDS, 0xa03);
-        return;
-    }
-    uint8_t* pages = (is_k ? P.k_pages : P.v_pages) + (long long)pid * page * P.Hkv * kKvD;
-    float* scale = (is_k ? P.k_scale : P.v_scale) + (long long)pid * P.Hkv + h0;
-    if (tid <= hmask) {
-        s_amax[tid] = 0u;
-        s_old[tid] = slot0 ? scale[tid] : 0.f;
-    }
     const unsigned long long turn = rope_turn(freq);
     auto position = [&](int t) {
         return static_cast<unsigned long long>(P.rope_pos ? (long long)P.rope_pos[S.i0 + t] : (long long)(S.p0 + t));
@@ -222,46 +223,80 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const AppendParams P) {
         for (int t = tfirst; t < tokens; t += tstep) {
             float c, s;
             rope_sincos(static_cast<uint32_t>((position(t) * turn) >> 32), c, s);
-            s_turn[t * n + pair] = make_float2(c * P.mscale, s * P.mscale);
+            s_turn[t * n + entry] = make_float2(c * P.mscale, s * P.mscale);
         }
+    }
+    if (pid < 0 || pid >= P.num_pages) {
+        if (tid == 0) record_error(DSA_DEV_ERR_BOUNDS, 0xa03);
+        return;
+    }
+    uint8_t* pages = (is_k ? P.k_pages : P.v_pages) + (long long)pid * page * P.Hkv * kKvD;
+    float* scale = (is_k ? P.k_scale : P.v_scale) + (long long)pid * P.Hkv + h0;
+    float old = 0.f;
+    if (tid <= hmask) {
+        s_amax[tid] = 0u;
+        old = slot0 ? scale[tid] : 0.f;  // consumed after the pass over the rows
     }
     __syncthreads();
 
-    // values in fp32: f[0..8) of vector a, f[8..16) of vector b
+    // the largest finite magnitude of this thread's rows, which are of one head.  Turned keys stay in fp32 from
+    // here on (f[0..8) of vector a, f[8..16) of vector b); values, and keys stored as they come, in bf16.
     float f[kAppendPasses][16];
     float m = 0.f;
     bool nan = false;
+    if (n) {
 #pragma unroll
-    for (int i = 0; i < kAppendPasses; ++i) {
-        const int r = row0 + i * step;
-        if (r >= rows) break;
-        float p[8], q[8];
-        RopeElem<__nv_bfloat16>::unpack(ra[i], p);
-        RopeElem<__nv_bfloat16>::unpack(rb[i], q);
-        if (turned) {
-            const float4* cs = reinterpret_cast<const float4*>(s_turn + (r >> hshift) * n + u * 8);
+        for (int i = 0; i < kAppendPasses; ++i) {
+            if (row0 + i * step >= rows) break;
+            float p[8], q[8];
+            RopeElem<__nv_bfloat16>::unpack(ra[i], p);
+            RopeElem<__nv_bfloat16>::unpack(rb[i], q);
+            if (turned) {
+                const float4* cs = reinterpret_cast<const float4*>(s_turn + ((row0 + i * step) >> hshift) * n) + u;
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const float4 t = cs[j / 2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int x = j + k;
-                    const float c = k ? t.z : t.x, s = k ? t.w : t.y;
+                for (int x = 0; x < 8; ++x) {
+                    const float4 t = cs[(x / 2) * turned_units];
+                    const float c = x & 1 ? t.z : t.x, s = x & 1 ? t.w : t.y;
                     const float e0 = INTER ? (x < 4 ? p[2 * x % 8] : q[2 * x % 8]) : p[x];
                     const float e1 = INTER ? (x < 4 ? p[(2 * x + 1) % 8] : q[(2 * x + 1) % 8]) : q[x];
-                    const float y0 = e0 * c - e1 * s, y1 = e0 * s + e1 * c;
-                    f[i][INTER ? 2 * x : x] = y0, f[i][INTER ? 2 * x + 1 : 8 + x] = y1;
+                    f[i][INTER ? 2 * x : x] = e0 * c - e1 * s, f[i][INTER ? 2 * x + 1 : 8 + x] = e0 * s + e1 * c;
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[i][j] = p[j], f[i][8 + j] = q[j];
             }
-        } else {
+            m = fmaxf(m, kv_amax(f[i]));
+            if (FMT == KV_INT8) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[i][j] = p[j], f[i][8 + j] = q[j];
+                for (int j = 0; j < 16; ++j) nan |= !(f[i][j] == f[i][j]);
+            }
         }
-        m = fmaxf(m, kv_amax(f[i]));
-        if (FMT == KV_INT8) {
+    } else {
+        __nv_bfloat162 most = __float2bfloat162_rn(0.f), seen = most;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) nan |= !(f[i][j] == f[i][j]);
+        for (int i = 0; i < kAppendPasses; ++i) {
+            if (row0 + i * step >= rows) break;
+            const uint32_t w[8] = {ra[i].x, ra[i].y, ra[i].z, ra[i].w, rb[i].x, rb[i].y, rb[i].z, rb[i].w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const __nv_bfloat162 v = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]));
+                most = __hmax2(most, v);  // passes NaN over
+                if (FMT == KV_INT8) seen = __hmax2_nan(seen, v);
+            }
         }
+        m = fmaxf(__low2float(most), __high2float(most));
+        if (m == INFINITY) {
+            m = 0.f;
+#pragma unroll
+            for (int i = 0; i < kAppendPasses; ++i) {
+                if (row0 + i * step >= rows) break;
+                float v[16];
+                RopeElem<__nv_bfloat16>::unpack(ra[i], *reinterpret_cast<float(*)[8]>(v));
+                RopeElem<__nv_bfloat16>::unpack(rb[i], *reinterpret_cast<float(*)[8]>(v + 8));
+                m = fmaxf(m, kv_amax(v));
+            }
+        }
+        nan = FMT == KV_INT8 && (__hisnan(__low2bfloat16(seen)) || __hisnan(__high2bfloat16(seen)));
     }
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -269,7 +304,8 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const AppendParams P) {
     if (FMT == KV_INT8 && nan) record_error(DSA_DEV_ERR_BOUNDS, 0xa04);
     __syncthreads();
     if (tid <= hmask) {
-        const float s = fmaxf(s_old[tid], kv_pow2(kv_exponent<FMT>(__uint_as_float(s_amax[tid]))));
+        const float s = fmaxf(old, kv_pow2(kv_exponent<FMT>(__uint_as_float(s_amax[tid]))));
+        s_old[tid] = old;
         s_new[tid] = s;
         scale[tid] = s;
     }
@@ -283,7 +319,14 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const AppendParams P) {
         const int r = row0 + i * step;
         if (r >= rows) break;
         uint32_t w[4];
-        if (!turned) {
+        if (!n) {
+            float v[16];
+            RopeElem<__nv_bfloat16>::unpack(ra[i], *reinterpret_cast<float(*)[8]>(v));
+            RopeElem<__nv_bfloat16>::unpack(rb[i], *reinterpret_cast<float(*)[8]>(v + 8));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = kv_round4<FMT>(v[4 * k] * inv, v[4 * k + 1] * inv, v[4 * k + 2] * inv, v[4 * k + 3] * inv);
+        } else if (!turned) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 w[k] = kv_round4<FMT>(f[i][4 * k] * inv, f[i][4 * k + 1] * inv, f[i][4 * k + 2] * inv, f[i][4 * k + 3] * inv);
@@ -291,20 +334,17 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const AppendParams P) {
             // pair x lies in bytes lo(x), hi(x); both ends of its error's interval are rounded.  The sine and
             // cosine are off by 2^-23 of 1 at most (their own ulp, the angle's rounding, mscale's), products and
             // sum by 2^-24, in all 2^-22.4 (|a| + |b|) <= 2^-21.9 (|y0| + |y1|).
-            float d[16];
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int lo = INTER ? 2 * x : x, hi = INTER ? 2 * x + 1 : 8 + x;
-                d[lo] = d[hi] = (fabsf(f[i][lo]) + fabsf(f[i][hi])) * inv * 4.76837158203125e-7f;  // 2^-21
-            }
+            const float eps = inv * 4.76837158203125e-7f;  // 2^-21
             unsigned differ[4], any = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float v[4], x[4];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    v[y] = fmaf(f[i][4 * k + y], inv, -d[4 * k + y]);
-                    x[y] = fmaf(f[i][4 * k + y], inv, d[4 * k + y]);
+                    const int e = 4 * k + y;
+                    const float d = (fabsf(f[i][e]) + fabsf(f[i][INTER ? e ^ 1 : e ^ 8])) * eps;
+                    v[y] = fmaf(f[i][e], inv, -d);
+                    x[y] = fmaf(f[i][e], inv, d);
                 }
                 w[k] = kv_round4<FMT>(v[0], v[1], v[2], v[3]);
                 differ[k] = w[k] ^ kv_round4<FMT>(x[0], x[1], x[2], x[3]);
@@ -313,14 +353,17 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const AppendParams P) {
             if (any) {
                 const __nv_bfloat16* at = in + (long long)(r >> hshift) * ts + my_h * hs;
                 const unsigned long long p = position(r >> hshift);
-#pragma unroll 1
+                unsigned todo = 0;  // pairs of which a byte differs
+#pragma unroll
                 for (int y = 0; y < 8; ++y) {
                     const int lo = INTER ? 2 * y : y, hi = INTER ? 2 * y + 1 : 8 + y;
+                    if ((differ[lo >> 2] >> (8 * (lo & 3)) | differ[hi >> 2] >> (8 * (hi & 3))) & 255u) todo |= 1u << y;
+                }
+#pragma unroll 1
+                for (; todo; todo &= todo - 1) {
+                    const int y = __ffs(todo) - 1;
+                    const int lo = INTER ? 2 * y : y, hi = INTER ? 2 * y + 1 : 8 + y;
                     const unsigned at_lo = 255u << (8 * (lo & 3)), at_hi = 255u << (8 * (hi & 3));
-                    unsigned dl = 0, dh = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) dl = lo >> 2 == k ? differ[k] : dl, dh = hi >> 2 == k ? differ[k] : dh;
-                    if (!((dl & at_lo) | (dh & at_hi))) continue;
                     double sd, cd;
                     const unsigned long long ph = p * rope_turn(P.inv_freq[u * 8 + y]);
                     sincospi(static_cast<double>(static_cast<long long>(ph)) * 1.0842021724855044e-19, &sd, &cd);  // 2^-63

@@ -46,16 +46,18 @@ __device__ __forceinline__ unsigned long long rope_turn(double inv_freq) {
 }
 
 // cos and sin of the angle phase / 2^32 turns.  The quadrant is taken off the integer, so that the
-// remainder keeps fp32's relative precision; about 1 ulp each.
+// remainder r, |r| <= pi / 4, keeps fp32's relative precision; Taylor's series to r^9 and r^10 then leave
+// 2^-28, and with fp32's roundings each result is off by 2^-23 at most.
 __device__ __forceinline__ void rope_sincos(uint32_t phase, float& c, float& s) {
     const uint32_t quad = (phase + 0x20000000u) >> 30;
-    const int rem = static_cast<int>(phase - (quad << 30));  // -2^29 .. 2^29 - 1
-    float sr, cr;
-    sincospif(static_cast<float>(rem) * 4.656612873077393e-10f, &sr, &cr);  // 2^-31: rem in units of pi
-    c = quad & 1 ? sr : cr;
-    s = quad & 1 ? cr : sr;
-    if (quad == 1 || quad == 2) c = -c;
-    if (quad >= 2) s = -s;
+    const float r = static_cast<float>(static_cast<int>(phase - (quad << 30))) * 1.4629180792671596e-9f;  // pi / 2^31
+    const float q = r * r;
+    const float ps = fmaf(q, fmaf(q, fmaf(q, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
+    const float pc = fmaf(q, fmaf(q, fmaf(q, fmaf(q, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f);
+    const float sr = fmaf(r * q, ps, r), cr = fmaf(q, pc, 1.f);
+    const bool odd = quad & 1;
+    c = __uint_as_float(__float_as_uint(odd ? sr : cr) ^ (((quad + 1) & 2) << 30));
+    s = __uint_as_float(__float_as_uint(odd ? cr : sr) ^ ((quad & 2) << 30));
 }
 
 // The same by the hardware's sine and cosine, whose absolute error on [-pi, pi] stays below 2^-21: for

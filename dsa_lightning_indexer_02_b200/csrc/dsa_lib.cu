@@ -540,25 +540,84 @@ cudaError_t launch_combine_t(const PagedParams& P, int TK, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, paged_combine_kernel<WPH>, P, TK);
 }
 
+template <int NT>
+cudaLaunchConfig_t paged_config(int64_t grid, int cluster, cudaLaunchAttribute* attr, cudaStream_t s) {
+    using C = PagedCfg<NT>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+// Clusters of `cluster` (2, 4 or 8) blocks of the attention kernel that fit on the device at once; 0 if the query
+// fails.  Asked once per device, kernel and size.
+template <int FMT, int NT, int HKV, bool IDX>
+int paged_clusters(int cluster, cudaStream_t s) {
+    static std::atomic<int> cache[kMaxDevices][4];  // 0: not asked yet
+    const int dev = current_device(), k = log2_of(cluster);
+    if (dev < 0) return 0;
+    int n = cache[dev][k].load(std::memory_order_relaxed);
+    if (!n) {
+        cudaLaunchAttribute attr[1];
+        const cudaLaunchConfig_t cfg = paged_config<NT>(cluster, cluster, attr, s);
+        if (cudaOccupancyMaxActiveClusters(&n, paged_attn_kernel<FMT, NT, HKV, IDX, true>, &cfg) != cudaSuccess || n <= 0) {
+            (void)cudaGetLastError();
+            n = -1;
+        }
+        cache[dev][k].store(n, std::memory_order_relaxed);
+    }
+    return n > 0 ? n : 0;
+}
+
 template <int FMT, int NT, int HKV, bool IDX>
 dsa_status launch_paged_t(PagedParams P, cudaStream_t s) {
     using C = PagedCfg<NT>;
-    auto kern = paged_attn_kernel<FMT, NT, HKV, IDX>;
-    static DeviceFlags attr_set;
-    if (!set_smem_limit(kern, C::SMEM, attr_set)) return DSA_ERR_CUDA;
+    auto dealt = paged_attn_kernel<FMT, NT, HKV, IDX, false>;
+    auto clustered = paged_attn_kernel<FMT, NT, HKV, IDX, true>;
+    static DeviceFlags dealt_set, clustered_set;
+    if (!set_smem_limit(dealt, C::SMEM, dealt_set) || !set_smem_limit(clustered, C::SMEM, clustered_set))
+        return DSA_ERR_CUDA;
     const int sms = num_sms();
     if (sms <= 0) return DSA_ERR_CUDA;
-    P.shared_rows = P.T <= kPagedSharedRows;
-    const int grid = P.shared_rows ? std::min(C::CTAS * sms, kPagedPartCtas) : P.T;
+    constexpr int TK = C::NW / HKV * C::KT * 16;
+    // Blocks of a row, in tiles of time: a cluster of c takes ceil(tiles / c) of them for as many rows at once
+    // as clusters fit; dealing by units takes the even share, and for its second kernel (4 us) as long as
+    // kJoinTiles.  Rows count with the most keys they can have.
+    const int64_t most = std::min<int64_t>((int64_t)P.max_pages << P.page_shift, P.idx ? P.topk : INT32_MAX);
+    const int64_t tiles = (most + TK - 1) / TK;
+    const int ctas = std::min(C::CTAS * sms, kPagedPartCtas);
+    constexpr int kJoinTiles = 5;
+    int64_t best = P.T <= kPagedSharedRows ? ((int64_t)P.T * (tiles + kPagedRowTiles) + ctas - 1) / ctas + kJoinTiles : INT64_MAX;
+    P.cluster = P.T <= kPagedSharedRows ? 0 : 1;
+    for (int c = 1; c <= 8; c *= 2) {
+        const int fit = c == 1 ? C::CTAS * sms : paged_clusters<FMT, NT, HKV, IDX>(c, s);
+        if (fit <= 0) continue;
+        const int64_t t = (P.T + fit - 1) / fit * ((tiles + c - 1) / c) + (c > 1);
+        if (t < best) best = t, P.cluster = c;
+    }
     {
         LaunchScope ls(K_PAGED_ATTN, s);
-        kern<<<grid, C::THREADS, C::SMEM, s>>>(P);
+        if (P.cluster == 0) {
+            dealt<<<ctas, C::THREADS, C::SMEM, s>>>(P);
+        } else {
+            cudaLaunchAttribute attr[1];
+            const cudaLaunchConfig_t cfg = paged_config<NT>((int64_t)P.T * P.cluster, P.cluster, attr, s);
+            if (cudaLaunchKernelEx(&cfg, clustered, P) != cudaSuccess) return DSA_ERR_CUDA;
+        }
         const dsa_status st = launch_status();
-        if (st != DSA_OK || !P.shared_rows) return st;
+        if (st != DSA_OK || P.cluster) return st;
     }
     // 8 warps on a head while there are few (row, head) pairs, down to one
     LaunchScope ls(K_COMBINE, s);
-    const int TK = C::NW / HKV * C::KT * 16, pairs = P.T * P.Hq;
+    const int pairs = P.T * P.Hq;
     const cudaError_t e = pairs <= 1184 ? launch_combine_t<8>(P, TK, s)
                           : pairs <= 2368 ? launch_combine_t<4>(P, TK, s)
                           : pairs <= 4736 ? launch_combine_t<2>(P, TK, s) : launch_combine_t<1>(P, TK, s);

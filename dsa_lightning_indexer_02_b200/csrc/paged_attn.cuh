@@ -21,14 +21,19 @@
 //     C takes units [c, c + 1) * ceil(U / C) of all rows' U, in order, whatever the rows' lengths.  A row that
 //     one block holds whole is finished there; of the others each block writes its unnormalised part, and
 //     paged_combine_kernel joins them.
+//   - Where that second kernel would cost more than even shares save (few keys, or rows enough to fill the
+//     GPU), a row gets a cluster of 1, 2, 4 or 8 blocks, which split its tiles evenly and join their outputs
+//     through each other's shared memory.
 #pragma once
+
+#include <type_traits>
 
 #include "kv8.cuh"
 
 namespace dsa {
 
 constexpr int kPagedPartCtas = 296;     // most blocks that share rows; each has two partial slots
-constexpr int kPagedSharedRows = 1184;  // with more rows, every row gets a block of its own
+constexpr int kPagedSharedRows = 1184;  // most rows that are dealt by units
 constexpr int kPagedPartStride = kKvD + 4;  // floats of a partial: O[128], max, sum, 2 pad
 constexpr int kPagedRowTiles = 1;       // what the end of a row costs a block, in tiles, when rows are dealt
 
@@ -44,7 +49,7 @@ struct PagedParams {
     float scale_log2;
     __nv_bfloat16* out;                // [T, Hq, 128]
     float* lse;                        // [T, Hq], may be null
-    int shared_rows;                   // rows are dealt by tiles (and joined); otherwise one block each
+    int cluster;                       // blocks of a row; 0: rows are dealt by units (and joined)
     float* part;                       // [2 * gridDim.x, Hq, kPagedPartStride]
     long long* row_start;              // [T + 1]: where the rows start, in units dealt; behind them a block's units
 };
@@ -83,6 +88,24 @@ __device__ __forceinline__ void cp_async_4(void* dst, const void* src, bool vali
     const int n = valid ? 4 : 0;
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
 }
+// The address of block `rank`'s counterpart of this block's shared-memory address, and reads of it.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -112,8 +135,8 @@ __device__ __forceinline__ void kv_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi)
     }
 }
 
-// IDX: keys named by idx; otherwise a step's 16 keys lie side by side in one page.
-template <int FMT, int NT, int HKV, bool IDX>
+// IDX: keys named by idx; otherwise a step's 16 keys lie side by side in one page.  CLU: P.cluster blocks a row.
+template <int FMT, int NT, int HKV, bool IDX, bool CLU>
 __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) paged_attn_kernel(const PagedParams P) {
     using C = PagedCfg<NT>;
     constexpr int NW = C::NW, S = C::S, KT = C::KT;
@@ -135,7 +158,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         paged_row(P, r, b, n);
         return (paged_count(P, n) + TK - 1) / TK;
     };
-    if (P.shared_rows && P.T <= 32) {
+    if (!CLU && P.T <= 32) {
         // every warp for itself, a row to a lane
         const int nt = lane < P.T ? row_tiles(lane) : 0, mine = nt ? nt + kPagedRowTiles : 0;
         int incl = mine;
@@ -158,7 +181,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         const int s0 = __shfl_sync(0xffffffffu, start, row0);
         tile0 = (int)max(0ll, w0 - s0);
         at = s0 + tile0;
-    } else if (P.shared_rows) {
+    } else if (!CLU) {
         __shared__ long long s_sum[NW], s_total, s_start;
         __shared__ int s_row0;
         const int per = (P.T + C::THREADS - 1) / C::THREADS;
@@ -211,14 +234,11 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         tile0 = (int)max(0ll, w0 - s_start);
         at = s_start + tile0;
     } else {
-        w1 = row_tiles(row0);
-        if (w1 == 0) {  // a row without keys
-            uint4* o = reinterpret_cast<uint4*>(P.out + (long long)row0 * P.Hq * kKvD);
-            for (int i = threadIdx.x; i < P.Hq * kKvD / 8; i += C::THREADS) o[i] = make_uint4(0, 0, 0, 0);
-            if (P.lse)
-                for (int h = threadIdx.x; h < P.Hq; h += C::THREADS) P.lse[(long long)row0 * P.Hq + h] = -INFINITY;
-            return;
-        }
+        row0 = blockIdx.x / P.cluster;
+        const int nt = row_tiles(row0), per = (nt + P.cluster - 1) / P.cluster;
+        tile0 = min(nt, (int)(blockIdx.x % P.cluster) * per);
+        w1 = min(nt, tile0 + per);
+        at = tile0;
     }
 
     uint8_t* ring = smem + warp * (S * C::STAGE);
@@ -234,8 +254,8 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     int f_nt = (paged_count(P, f_n) + TK - 1) / TK;
     const int my_key = IDX ? (KT == 2 ? lane : lane & 15) : (lane & 15) * 16;
     const bool has_key = IDX || (lane & 15) < KT;
-    int a_key = -1, a_n = 0, a_b = 0;  // numbers loaded
-    int b_slot = -1, b_valid = 0;      // pages looked up: token's slot in the pool, -1 none; keys from it on
+    int a_key = -1, a_n = 0, a_b = 0;   // numbers loaded
+    int b_key = -1, b_n = 0, b_pid = 0; // pages looked up; nothing waits for the page number before the copy
     auto load_keys = [&]() {
         a_key = -1;
         if (f_at >= w1) return;
@@ -255,16 +275,8 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         }
     };
     auto look_up = [&]() {
-        b_slot = -1, b_valid = 0;
-        if (a_key >= 0 && a_key < a_n) {
-            const int pid = P.table[(long long)a_b * P.max_pages + (a_key >> P.page_shift)];
-            if (pid < 0 || pid >= P.num_pages) {
-                record_error(DSA_DEV_ERR_BOUNDS, 0xb02);
-            } else {
-                b_slot = (pid << P.page_shift) + (a_key & ((1 << P.page_shift) - 1));
-                b_valid = min(16, a_n - a_key);
-            }
-        }
+        b_key = a_key < a_n ? a_key : -1, b_n = a_n;
+        if (b_key >= 0) b_pid = P.table[(long long)a_b * P.max_pages + (b_key >> P.page_shift)];
     };
     // lane's part of every row copy: row lane / 8 of four, 16-byte chunk lane % 8
     const uint8_t* k_lane = P.k_pages + head * kKvD + (lane & 7) * 16 + (IDX ? 0 : (lane >> 3) * ROWB);
@@ -275,6 +287,16 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         uint8_t* dst = ring + st * C::STAGE + lr * kKvD;
         // row r = 4 i + lr of a tile: K's chunk c goes to c ^ 4 (r & 1), V's to c ^ (r & 6)
         const int k_at = (lc ^ ((lr & 1) << 2)) << 4;
+        // the token's slot in the pool (-1: none) and the keys from it on
+        int b_slot = -1, b_valid = 0;
+        if (b_key >= 0) {
+            if (b_pid < 0 || b_pid >= P.num_pages) {
+                record_error(DSA_DEV_ERR_BOUNDS, 0xb02);
+            } else {
+                b_slot = (b_pid << P.page_shift) + (b_key & ((1 << P.page_shift) - 1));
+                b_valid = min(16, b_n - b_key);
+            }
+        }
         if constexpr (IDX) {
             const unsigned mask = __ballot_sync(0xffffffffu, b_slot >= 0);
             if (lane == 0) reinterpret_cast<unsigned*>(sc)[C::META - 1] = mask;
@@ -319,16 +341,6 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         }
         cp_async_commit();
     };
-    load_keys();
-    look_up();
-    load_keys();
-#pragma unroll
-    for (int s = 0; s < S - 1; ++s) {
-        copy_rows(s);
-        look_up();
-        load_keys();
-    }
-
     // ---- per row: queries, running maximum, sums, outputs
     uint32_t qf[NT][8][2];
     float qfac[NT][2];  // of heads nt * 8 + 2 j + {0, 1}: logits in log2 per unit of the product
@@ -336,21 +348,28 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     int row = row0, left;  // left: tiles of the row still to come in this block
     bool whole;            // the block holds the row from its first tile to its last
     int slot;              // where its part goes if not: 0 where the row reaches back to the block's first unit
-    auto begin_row = [&](int tile) {
-        int b, n;
-        paged_row(P, row, b, n);
+    uint2 q_raw[NT][8];
+    auto load_q = [&]() {
+#pragma unroll
+        for (int nt8 = 0; nt8 < NT; ++nt8) {
+            const int hl = nt8 * 8 + g;
+            const __nv_bfloat16* qrow = P.q + ((long long)row * P.Hq + head * G + (hl < G ? hl : 0)) * kKvD;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+                q_raw[nt8][kk] = *reinterpret_cast<const uint2*>(qrow + (kk < 4 ? j * 16 + kk * 4 : 64 + j * 16 + (kk - 4) * 4));
+        }
+    };
+    auto begin_row = [&](int tile, int n) {  // after load_q
         const int nt = (paged_count(P, n) + TK - 1) / TK;
         left = (int)min((long long)(nt - tile), w1 - at);
         whole = tile == 0 && left == nt;
         slot = at - tile <= w0 ? 0 : 1;
 #pragma unroll
         for (int nt8 = 0; nt8 < NT; ++nt8) {
-            const int hl = nt8 * 8 + g;
-            const __nv_bfloat16* qrow = P.q + ((long long)row * P.Hq + head * G + (hl < G ? hl : 0)) * kKvD;
             float f[8][4], top = 0.f;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
-                const uint2 w = *reinterpret_cast<const uint2*>(qrow + (kk < 4 ? j * 16 + kk * 4 : 64 + j * 16 + (kk - 4) * 4));
+                const uint2 w = q_raw[nt8][kk];
                 f[kk][0] = __uint_as_float(w.x << 16), f[kk][1] = __uint_as_float(w.x & 0xffff0000u);
                 f[kk][2] = __uint_as_float(w.y << 16), f[kk][3] = __uint_as_float(w.y & 0xffff0000u);
 #pragma unroll
@@ -361,7 +380,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
             // 2^s brings the head's largest below 2^14
             int s = 13 - ((int)(__float_as_uint(top) >> 23) - 127);
             s = max(-114, min(100, s));
-            const float up = hl < G ? kv_pow2(s) : 0.f;
+            const float up = nt8 * 8 + g < G ? kv_pow2(s) : 0.f;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
                 qf[nt8][kk][0] = pack_f16x2(f[kk][0] * up, f[kk][1] * up);
@@ -379,9 +398,82 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                 for (int i = 0; i < 4; ++i) o[nt8][dt][i] = 0.f;
         }
     };
-    begin_row(tile0);
+    {
+        const int n0 = f_n;  // of row0
+        load_keys();
+        look_up();
+        load_q();
+        load_keys();
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s) {
+            copy_rows(s);
+            look_up();
+            load_keys();
+        }
+        begin_row(tile0, n0);
+    }
 
-    for (int st = 0;;) {
+    // This warp's outputs, maxima and sums to shared memory: fragments [nt * 8 + dt][lane][4] in ring stage st,
+    // (two maxima, two sums) as [nt][j] in xch.
+    auto leave = [&](int st) {
+        float4* frag = reinterpret_cast<float4*>(ring + st * C::STAGE) + lane;
+        float4* ml = reinterpret_cast<float4*>(xch) + warp * (NT * 4) + j;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float l = l_run[nt][x];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                l_run[nt][x] = l;
+            }
+            if (g == 0) ml[nt * 4] = make_float4(m_run[nt][0], m_run[nt][1], l_run[nt][0], l_run[nt][1]);
+#pragma unroll
+            for (int dt = 0; dt < 8; ++dt) frag[(nt * 8 + dt) * 32] = make_float4(o[nt][dt][0], o[nt][dt][1], o[nt][dt][2], o[nt][dt][3]);
+        }
+    };
+    // A fragment of the row's output: weights and adds what `parts` of at most MOST warps (or blocks) left, and
+    // writes dims 16 g + 2 dt, + 1 of heads nt * 8 + 2 j, + 1.  max_sum(p) gives part p's maxima and sums of the
+    // two heads, value(p) its fragment.
+    auto join = [&](auto most, int nt, int dt, int parts, auto max_sum, auto value) {
+        constexpr int MOST = decltype(most)::value;
+        float2 m = make_float2(kPagedNone, kPagedNone), l = make_float2(0.f, 0.f);
+        float a[4] = {0.f, 0.f, 0.f, 0.f};
+        float4 t[MOST], v[MOST];
+#pragma unroll
+        for (int p = 0; p < MOST; ++p)
+            if (p < parts) t[p] = max_sum(p), v[p] = value(p);
+#pragma unroll
+        for (int p = 0; p < MOST; ++p)
+            if (p < parts) m.x = fmaxf(m.x, t[p].x), m.y = fmaxf(m.y, t[p].y);
+#pragma unroll
+        for (int p = 0; p < MOST; ++p) {
+            if (p >= parts) continue;
+            const float wx = exp2f(t[p].x - m.x), wy = exp2f(t[p].y - m.y);
+            l.x += t[p].z * wx, l.y += t[p].w * wy;
+            a[0] += v[p].x * wx, a[1] += v[p].y * wy, a[2] += v[p].z * wx, a[3] += v[p].w * wy;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int hl = nt * 8 + 2 * j + x;
+            if (hl >= G) continue;
+            const long long h = (long long)row * P.Hq + head * G + hl;
+            const float mx = x ? m.y : m.x, lx = x ? l.y : l.x;
+            if (whole) {
+                const float inv = lx == 0.f ? 0.f : 1.f / lx;
+                *reinterpret_cast<uint32_t*>(P.out + h * kKvD + 16 * g + 2 * dt) = pack_bf16x2(a[x] * inv, a[2 + x] * inv);
+                if (P.lse && g == 0 && dt == 0) P.lse[h] = lx == 0.f ? -INFINITY : (mx + log2f(lx)) * 0.69314718055994531f;
+            } else {
+                float* part = P.part + ((2ll * blockIdx.x + slot) * P.Hq + head * G + hl) * kPagedPartStride;
+                *reinterpret_cast<float2*>(part + 16 * g + 2 * dt) = make_float2(a[x], a[2 + x]);
+                if (g == 0 && dt == 0) *reinterpret_cast<float2*>(part + kKvD) = make_float2(mx, lx);
+            }
+        }
+    };
+
+    int used = 0;
+    for (int st = 0; at < w1;) {
         cp_async_wait<S - 2>();
         __syncwarp();
         copy_rows(st == 0 ? S - 1 : st - 1);  // the stage that the last iteration used up
@@ -528,74 +620,92 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                 }
             }
         }
-        const int used = st;
+        used = st;
         st = st + 1 == S ? 0 : st + 1;
         ++at;
         if (--left) continue;
 
         // ---- the row's last tile in this block: the warps of a KV head exchange their outputs through the
         // stages that they have just used up, and each joins and writes every NSUB-th fragment
-        float* frag = reinterpret_cast<float*>(ring + used * C::STAGE) + lane;
-        float* ml = xch + warp * (NT * 16);  // [nt][maximum, sum][j][column]
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float l = l_run[nt][x];
-                l += __shfl_xor_sync(0xffffffffu, l, 4);
-                l += __shfl_xor_sync(0xffffffffu, l, 8);
-                l += __shfl_xor_sync(0xffffffffu, l, 16);
-                if (g == 0) ml[nt * 16 + j * 2 + x] = m_run[nt][x], ml[nt * 16 + 8 + j * 2 + x] = l;
-            }
-#pragma unroll
-            for (int dt = 0; dt < 8; ++dt)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) frag[((nt * 8 + dt) * 4 + x) * 32] = o[nt][dt][x];
-        }
+        if (CLU && P.cluster > 1) break;
+        leave(used);
         __syncthreads();
 #pragma unroll 1
         for (int i = sub; i < NT * 8; i += NSUB) {
-            const int nt = i >> 3, dt = i & 7;
-            const float2* mlh = reinterpret_cast<const float2*>(xch + head * (NT * 16) + nt * 16) + j;
-            float2 m = make_float2(kPagedNone, kPagedNone), l = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < NSUB; ++w) {
-                const float2 t = mlh[w * HKV * (NT * 8)];
-                m.x = fmaxf(m.x, t.x), m.y = fmaxf(m.y, t.y);
-            }
-            float a[4] = {0.f, 0.f, 0.f, 0.f};
-            const float* src = reinterpret_cast<const float*>(smem + head * (S * C::STAGE) + used * C::STAGE) + (nt * 8 + dt) * 128 + lane;
-#pragma unroll
-            for (int w = 0; w < NSUB; ++w) {
-                const float2 t = mlh[w * HKV * (NT * 8)], u = mlh[w * HKV * (NT * 8) + 4];
-                const float wx = exp2f(t.x - m.x), wy = exp2f(t.y - m.y);
-                l.x += u.x * wx, l.y += u.y * wy;
-                const float* p = src + w * HKV * (S * C::STAGE / 4);
-                a[0] += p[0] * wx, a[1] += p[32] * wy, a[2] += p[64] * wx, a[3] += p[96] * wy;
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int hl = nt * 8 + 2 * j + x;
-                if (hl >= G) continue;
-                const long long h = (long long)row * P.Hq + head * G + hl;
-                const float mx = x ? m.y : m.x, lx = x ? l.y : l.x;
-                if (whole) {
-                    const float inv = lx == 0.f ? 0.f : 1.f / lx;
-                    *reinterpret_cast<uint32_t*>(P.out + h * kKvD + 16 * g + 2 * dt) = pack_bf16x2(a[x] * inv, a[2 + x] * inv);
-                    if (P.lse && g == 0 && dt == 0) P.lse[h] = lx == 0.f ? -INFINITY : (mx + log2f(lx)) * 0.69314718055994531f;
-                } else {
-                    float* part = P.part + ((2ll * blockIdx.x + slot) * P.Hq + head * G + hl) * kPagedPartStride;
-                    *reinterpret_cast<float2*>(part + 16 * g + 2 * dt) = make_float2(a[x], a[2 + x]);
-                    if (g == 0 && dt == 0) *reinterpret_cast<float2*>(part + kKvD) = make_float2(mx, lx);
-                }
-            }
+            const float4* ml = reinterpret_cast<const float4*>(xch) + head * (NT * 4) + (i >> 3) * 4 + j;
+            const float4* src = reinterpret_cast<const float4*>(smem + head * (S * C::STAGE) + used * C::STAGE) + i * 32 + lane;
+            join(
+                std::integral_constant<int, NSUB>(), i >> 3, i & 7, NSUB, [&](int p) { return ml[p * HKV * (NT * 4)]; },
+                [&](int p) { return src[p * HKV * (S * C::STAGE / 16)]; });
         }
+        if (CLU) break;
         at += kPagedRowTiles;
         if (at >= w1) break;
-        do ++row;
-        while (row_tiles(row) == 0);
-        begin_row(0);
+        int b, n;
+        do paged_row(P, ++row, b, n);
+        while (paged_count(P, n) == 0);
+        load_q();
+        begin_row(0, n);
         __syncthreads();  // the stages are read: the next copies may take them
+    }
+    if (CLU && P.cluster == 1 && w1 == 0) {  // a row without keys
+        uint4* o = reinterpret_cast<uint4*>(P.out + (long long)row0 * P.Hq * kKvD);
+        for (int i = threadIdx.x; i < P.Hq * kKvD / 8; i += C::THREADS) o[i] = make_uint4(0, 0, 0, 0);
+        if (P.lse)
+            for (int h = threadIdx.x; h < P.Hq; h += C::THREADS) P.lse[(long long)row0 * P.Hq + h] = -INFINITY;
+    }
+    if (CLU && P.cluster > 1) {
+        // ---- the blocks of a cluster join the row: first each the fragments of its own warps, into the stages of
+        // its first warps, then one warp of one block each fragment from all blocks
+        __syncwarp();
+        leave(0);
+        __syncthreads();
+        float4 all[NT];  // maxima and sums over this block's warps of the head
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float4* ml = reinterpret_cast<const float4*>(xch) + head * (NT * 4) + nt * 4 + j;
+            float4 w[NSUB];
+            all[nt] = make_float4(kPagedNone, kPagedNone, 0.f, 0.f);
+#pragma unroll
+            for (int p = 0; p < NSUB; ++p) {
+                w[p] = ml[p * HKV * (NT * 4)];
+                all[nt].x = fmaxf(all[nt].x, w[p].x), all[nt].y = fmaxf(all[nt].y, w[p].y);
+            }
+#pragma unroll
+            for (int p = 0; p < NSUB; ++p) {
+                w[p].x = exp2f(w[p].x - all[nt].x), w[p].y = exp2f(w[p].y - all[nt].y);
+                all[nt].z += w[p].z * w[p].x, all[nt].w += w[p].w * w[p].y;
+            }
+#pragma unroll
+            for (int dt = 0; dt < 8; ++dt) {
+                if ((nt * 8 + dt) % NSUB != sub) continue;  // each fragment by one warp
+                float4* at = reinterpret_cast<float4*>(smem + head * (S * C::STAGE)) + (nt * 8 + dt) * 32 + lane;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int p = 0; p < NSUB; ++p) {
+                    const float4 v = at[p * HKV * (S * C::STAGE / 16)];
+                    a.x += v.x * w[p].x, a.y += v.y * w[p].y, a.z += v.z * w[p].x, a.w += v.w * w[p].y;
+                }
+                *at = a;
+            }
+        }
+        __syncthreads();  // the warps' maxima are read
+        if (sub == 0 && g == 0) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) reinterpret_cast<float4*>(xch)[head * (NT * 4) + nt * 4 + j] = all[nt];
+        }
+        cluster_sync();
+        whole = true;
+        const int rank = blockIdx.x % P.cluster;
+#pragma unroll 1
+        for (int i = sub * P.cluster + rank; i < NT * 8; i += NSUB * P.cluster) {
+            const uint32_t ml = smem_u32(reinterpret_cast<const float4*>(xch) + head * (NT * 4) + (i >> 3) * 4 + j);
+            const uint32_t src = smem_u32(reinterpret_cast<const float4*>(smem + head * (S * C::STAGE)) + i * 32 + lane);
+            join(
+                std::integral_constant<int, 8>(), i >> 3, i & 7, P.cluster, [&](int p) { return ld_cluster(cluster_addr(ml, p)); },
+                [&](int p) { return ld_cluster(cluster_addr(src, p)); });
+        }
+        cluster_sync();  // no block leaves while another reads its shared memory
     }
 }
 

@@ -8,10 +8,11 @@
 //     that no barrier stands between copies and products and every SM keeps 16 rings in flight.
 //     Dense rows and selected keys differ only in where a lane's key number comes from.
 //   - Both products run on fp16 matrix instructions, where e4m3 and int8 values are exact:
-//     S^T[keys x heads] = K Q^T and O^T += V^T P^T, the G query heads of the KV head as columns.  The rows
-//     of the fragments stand for whichever keys and dims make a thread's bytes adjacent, so K and V go
-//     from shared memory to fragments by 16-byte loads; K's 16-byte chunks are exchanged by key parity
-//     and V's by key pair, which keeps those loads free of bank conflicts.
+//     S^T[keys x heads] = K Q^T and O^T += V^T P^T, the G query heads of the KV head as columns.  The rows of
+//     K's fragments stand for whichever dims make a thread's bytes adjacent, so K goes from shared memory by
+//     16-byte loads; V's fragments come transposed as bytes, their columns keys 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of
+//     a tile, as S leaves them.  K's 16-byte chunks are exchanged by key parity, V's by f(key) = key mod 4 +
+//     4 (key / 8 mod 2), which keeps these reads free of bank conflicts.
 //   - q goes to fp16 after its head is scaled by a power of two to at most 2^14: no bit of bf16's is lost
 //     within 2^-28 of the head's largest.
 //   - V's scale 2^e * m, 1 <= m < 2, enters through the exponent: the softmax's reference is the running
@@ -68,7 +69,9 @@ struct PagedCfg {
     static constexpr int META_BYTES = NW * S * META * 4;
     static constexpr int XCH_BYTES = NW * NT * 16 * 4;  // maxima and sums of a warp's heads
     static_assert(NT * 8 * 4 * 32 * 4 <= STAGE, "a warp's outputs are exchanged through one of its stages");
-    static constexpr int SMEM = RING_BYTES + META_BYTES + XCH_BYTES;
+    // two groups' queries would not leave registers for 12 warps: they are read from shared memory, [KV head][k][lane]
+    static constexpr int Q_BYTES = NT == 2 ? 4 * 8 * 32 * 16 : 0;
+    static constexpr int SMEM = RING_BYTES + META_BYTES + XCH_BYTES + Q_BYTES;
 };
 constexpr float kPagedNone = -1e30f;  // the running maximum before any key
 
@@ -112,6 +115,13 @@ __device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint32_t (&a)
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two 16 x 16 byte matrices (lane i gives row i's address), transposed: thread (g, j) gets column g's and g + 8's
+// bytes of rows 4 j .. 4 j + 3 of the first, then of the second.
+__device__ __forceinline__ void ldmatrix_b8_x2_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -241,15 +251,20 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         at = tile0;
     }
 
+    // from here on units count from w0: the block's are [0, units), the next one `now`
+    const int units = (int)(w1 - w0);
+    int now = (int)(at - w0);
+
     uint8_t* ring = smem + warp * (S * C::STAGE);
     float* meta = reinterpret_cast<float*>(smem + C::RING_BYTES) + warp * (S * C::META);
     float* xch = reinterpret_cast<float*>(smem + C::RING_BYTES + C::META_BYTES);
+    uint4* q_sh = reinterpret_cast<uint4*>(smem + C::RING_BYTES + C::META_BYTES + C::XCH_BYTES) + head * (8 * 32) + lane;
 
     // ---- copies.  A step's keys pass three stages, one iteration apart: their numbers are loaded, their
     // pages looked up, their rows copied.  With IDX lane i has key i of the step (KT = 1: i mod 16);
     // otherwise lane i has the first key of 16-key tile i mod 16, for i mod 16 < KT.
     int f_row = row0, f_tile = tile0, f_b, f_n;  // front cursor: the next tile whose keys are loaded
-    long long f_at = at;
+    int f_at = now;
     paged_row(P, f_row, f_b, f_n);
     int f_nt = (paged_count(P, f_n) + TK - 1) / TK;
     const int my_key = IDX ? (KT == 2 ? lane : lane & 15) : (lane & 15) * 16;
@@ -258,7 +273,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     int b_key = -1, b_n = 0, b_pid = 0; // pages looked up; nothing waits for the page number before the copy
     auto load_keys = [&]() {
         a_key = -1;
-        if (f_at >= w1) return;
+        if (f_at >= units) return;
         const int e = f_tile * TK + sub * (KT * 16) + my_key;
         a_n = f_n, a_b = f_b;
         if (has_key && e < paged_count(P, f_n)) a_key = IDX ? P.idx[(long long)f_row * P.topk + e] : e;
@@ -266,7 +281,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         if (++f_tile == f_nt) {
             f_at += kPagedRowTiles;
             f_tile = 0;
-            if (f_at < w1) {  // some later row has units before w1
+            if (f_at < units) {  // some later row has units of this block
                 do {
                     paged_row(P, ++f_row, f_b, f_n);
                     f_nt = (paged_count(P, f_n) + TK - 1) / TK;
@@ -285,7 +300,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     auto copy_rows = [&](int st) {
         float* sc = meta + st * C::META;
         uint8_t* dst = ring + st * C::STAGE + lr * kKvD;
-        // row r = 4 i + lr of a tile: K's chunk c goes to c ^ 4 (r & 1), V's to c ^ (r & 6)
+        // row r = 4 i + lr of a tile: K's chunk c goes to c ^ 4 (r & 1), V's to c ^ f(r)
         const int k_at = (lc ^ ((lr & 1) << 2)) << 4;
         // the token's slot in the pool (-1: none) and the keys from it on
         int b_slot = -1, b_valid = 0;
@@ -307,7 +322,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                     const int s = __shfl_sync(0xffffffffu, b_slot, r);
                     const bool ok = s >= 0;
                     const long long at = ok ? (long long)s * ROWB : 0;
-                    const int v_at = (lc ^ (((i & 1) << 2) | (lr & 2))) << 4;
+                    const int v_at = (lc ^ (lr | (i & 2) << 1)) << 4;
                     cp_async_16(dst + (i >> 2) * 4096 + (i & 3) * 512 + k_at, k_lane + at, ok);
                     cp_async_16(dst + (i >> 2) * 4096 + 2048 + (i & 3) * 512 + v_at, v_lane + at, ok);
                 }
@@ -321,18 +336,24 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                 }
             }
         } else {
+            int s[KT], n[KT], all = 0;
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
-                const int s = __shfl_sync(0xffffffffu, b_slot, t), n = __shfl_sync(0xffffffffu, b_valid, t);
-                if (lane == 0) reinterpret_cast<int*>(sc)[C::META - 1 - t] = n;
-                if (n == 0) continue;
-                const long long at = (long long)s * ROWB;
+                s[t] = __shfl_sync(0xffffffffu, b_slot, t), n[t] = __shfl_sync(0xffffffffu, b_valid, t);
+                if (lane == 0) reinterpret_cast<int*>(sc)[C::META - 1 - t] = n[t];
+                all |= n[t];
+            }
+            if (all) {  // a tile without keys is filled with zeros if the step's other one has some
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool ok = n == 16 || i * 4 + lr < n;
-                    const int v_at = (lc ^ (((i & 1) << 2) | (lr & 2))) << 4;
-                    cp_async_16(dst + t * 4096 + i * 512 + k_at, k_lane + at + i * 4 * ROWB, ok);
-                    cp_async_16(dst + t * 4096 + 2048 + i * 512 + v_at, v_lane + at + i * 4 * ROWB, ok);
+                for (int t = 0; t < KT; ++t) {
+                    const long long at = n[t] ? (long long)s[t] * ROWB : 0;  // a tile's 16 slots are in the pool, filled or not
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool ok = i * 4 + lr < n[t];
+                        const int v_at = (lc ^ (lr | (i & 2) << 1)) << 4;
+                        cp_async_16(dst + t * 4096 + i * 512 + k_at, k_lane + at + i * 4 * ROWB, ok);
+                        cp_async_16(dst + t * 4096 + 2048 + i * 512 + v_at, v_lane + at + i * 4 * ROWB, ok);
+                    }
                 }
             }
             if (has_key && b_valid)
@@ -342,8 +363,9 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         cp_async_commit();
     };
     // ---- per row: queries, running maximum, sums, outputs
-    uint32_t qf[NT][8][2];
-    float qfac[NT][2];  // of heads nt * 8 + 2 j + {0, 1}: logits in log2 per unit of the product
+    uint32_t qf[NT == 1 ? 8 : 1][2];
+    float qfac[NT][2];     // of heads nt * 8 + 2 j + {0, 1}: logits in log2 per unit of the product
+    bool started = false;  // this warp has seen a key of the row: m_run holds maxima
     float o[NT][8][4], m_run[NT][2], l_run[NT][2];
     int row = row0, left;  // left: tiles of the row still to come in this block
     bool whole;            // the block holds the row from its first tile to its last
@@ -361,9 +383,10 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     };
     auto begin_row = [&](int tile, int n) {  // after load_q
         const int nt = (paged_count(P, n) + TK - 1) / TK;
-        left = (int)min((long long)(nt - tile), w1 - at);
+        left = min(nt - tile, units - now);
         whole = tile == 0 && left == nt;
-        slot = at - tile <= w0 ? 0 : 1;
+        slot = now <= tile ? 0 : 1;
+        started = false;
 #pragma unroll
         for (int nt8 = 0; nt8 < NT; ++nt8) {
             float f[8][4], top = 0.f;
@@ -383,14 +406,15 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
             const float up = nt8 * 8 + g < G ? kv_pow2(s) : 0.f;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk) {
-                qf[nt8][kk][0] = pack_f16x2(f[kk][0] * up, f[kk][1] * up);
-                qf[nt8][kk][1] = pack_f16x2(f[kk][2] * up, f[kk][3] * up);
+                const uint2 w = make_uint2(pack_f16x2(f[kk][0] * up, f[kk][1] * up), pack_f16x2(f[kk][2] * up, f[kk][3] * up));
+                if constexpr (NT == 1) qf[kk][0] = w.x, qf[kk][1] = w.y;
+                else if (sub == 0) reinterpret_cast<uint2*>(q_sh + kk * 32)[nt8] = w;
             }
             const float fac = P.scale_log2 * kv_pow2(-s);
 #pragma unroll
             for (int jj = 0; jj < 2; ++jj) {
                 qfac[nt8][jj] = __shfl_sync(0xffffffffu, fac, (2 * j + jj) * 4);
-                m_run[nt8][jj] = kPagedNone, l_run[nt8][jj] = 0.f;
+                m_run[nt8][jj] = 0.f, l_run[nt8][jj] = 0.f;
             }
 #pragma unroll
             for (int dt = 0; dt < 8; ++dt)
@@ -411,6 +435,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
             load_keys();
         }
         begin_row(tile0, n0);
+        if (NT == 2) __syncthreads();  // the queries are in shared memory
     }
 
     // This warp's outputs, maxima and sums to shared memory: fragments [nt * 8 + dt][lane][4] in ring stage st,
@@ -428,13 +453,14 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 l_run[nt][x] = l;
             }
-            if (g == 0) ml[nt * 4] = make_float4(m_run[nt][0], m_run[nt][1], l_run[nt][0], l_run[nt][1]);
+            if (g == 0)
+                ml[nt * 4] = make_float4(started ? m_run[nt][0] : kPagedNone, started ? m_run[nt][1] : kPagedNone, l_run[nt][0], l_run[nt][1]);
 #pragma unroll
             for (int dt = 0; dt < 8; ++dt) frag[(nt * 8 + dt) * 32] = make_float4(o[nt][dt][0], o[nt][dt][1], o[nt][dt][2], o[nt][dt][3]);
         }
     };
     // A fragment of the row's output: weights and adds what `parts` of at most MOST warps (or blocks) left, and
-    // writes dims 16 g + 2 dt, + 1 of heads nt * 8 + 2 j, + 1.  max_sum(p) gives part p's maxima and sums of the
+    // writes dims 16 dt + g, + 8 of heads nt * 8 + 2 j, + 1 (a lane and the next one pair theirs to adjacent dims).  max_sum(p) gives part p's maxima and sums of the
     // two heads, value(p) its fragment.
     auto join = [&](auto most, int nt, int dt, int parts, auto max_sum, auto value) {
         constexpr int MOST = decltype(most)::value;
@@ -454,26 +480,33 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
             l.x += t[p].z * wx, l.y += t[p].w * wy;
             a[0] += v[p].x * wx, a[1] += v[p].y * wy, a[2] += v[p].z * wx, a[3] += v[p].w * wy;
         }
+        const bool odd = g & 1;
+        const int dim = 16 * dt + (g & 6) + (odd ? 8 : 0);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int hl = nt * 8 + 2 * j + x;
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? a[x] : a[2 + x], 4);
+            const float v0 = odd ? other : a[x], v1 = odd ? a[2 + x] : other;  // dims dim, dim + 1
             if (hl >= G) continue;
             const long long h = (long long)row * P.Hq + head * G + hl;
             const float mx = x ? m.y : m.x, lx = x ? l.y : l.x;
             if (whole) {
                 const float inv = lx == 0.f ? 0.f : 1.f / lx;
-                *reinterpret_cast<uint32_t*>(P.out + h * kKvD + 16 * g + 2 * dt) = pack_bf16x2(a[x] * inv, a[2 + x] * inv);
+                *reinterpret_cast<uint32_t*>(P.out + h * kKvD + dim) = pack_bf16x2(v0 * inv, v1 * inv);
                 if (P.lse && g == 0 && dt == 0) P.lse[h] = lx == 0.f ? -INFINITY : (mx + log2f(lx)) * 0.69314718055994531f;
             } else {
                 float* part = P.part + ((2ll * blockIdx.x + slot) * P.Hq + head * G + hl) * kPagedPartStride;
-                *reinterpret_cast<float2*>(part + 16 * g + 2 * dt) = make_float2(a[x], a[2 + x]);
+                *reinterpret_cast<float2*>(part + dim) = make_float2(v0, v1);
                 if (g == 0 && dt == 0) *reinterpret_cast<float2*>(part + kKvD) = make_float2(mx, lx);
             }
         }
     };
 
+    // V's row of this lane in a transposed load: lane 16 t + 4 a + b gives key 2 a + (b & 1) + 8 (b >> 1) of tile t
+    const int v_row = (lane >> 4) * 4096 + 2048 + (((lane >> 2) & 3) * 2 + (lane & 1) + (lane & 2) * 4) * kKvD;
+    const int v_swz = (lane & 1) | ((lane >> 2) & 1) << 1 | (lane & 2) << 1;
     int used = 0;
-    for (int st = 0; at < w1;) {
+    for (int st = 0; now < units;) {
         cp_async_wait<S - 2>();
         __syncwarp();
         copy_rows(st == 0 ? S - 1 : st - 1);  // the stage that the last iteration used up
@@ -495,28 +528,41 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
             const uint8_t* k0 = stage + g * kKvD + ((j ^ ((g & 1) << 2)) << 4);
             const uint8_t* k1 = stage + g * kKvD + ((j ^ ((g & 1) << 2) ^ 4) << 4);
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
+            for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) z[t][nt][x] = 0.f;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < 2; ++half) {
+                uint32_t xw[KT][4], yw[KT][4];
+#pragma unroll
+                for (int t = 0; t < KT; ++t) {
                     const uint8_t* p = (half ? k1 : k0) + t * 4096;
                     const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 8 * kKvD);
-                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+                    xw[t][0] = x.x, xw[t][1] = x.y, xw[t][2] = x.z, xw[t][3] = x.w;
+                    yw[t][0] = y.x, yw[t][1] = y.y, yw[t][2] = y.z, yw[t][3] = y.w;
+                }
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t q[NT][2];
+                    if constexpr (NT == 1) {
+                        q[0][0] = qf[half * 4 + w][0], q[0][1] = qf[half * 4 + w][1];
+                    } else {
+                        const uint4 v = q_sh[(half * 4 + w) * 32];
+                        q[0][0] = v.x, q[0][1] = v.y, q[NT - 1][0] = v.z, q[NT - 1][1] = v.w;
+                    }
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) {
                         uint32_t a[4];
-                        kv_f16x4<FMT>(xw[w], a[0], a[2]);
-                        kv_f16x4<FMT>(yw[w], a[1], a[3]);
+                        kv_f16x4<FMT>(xw[t][w], a[0], a[2]);
+                        kv_f16x4<FMT>(yw[t][w], a[1], a[3]);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_16816_f16(z[t][nt], a, qf[nt][half * 4 + w][0], qf[nt][half * 4 + w][1]);
+                        for (int nt = 0; nt < NT; ++nt) mma_16816_f16(z[t][nt], a, q[nt][0], q[nt][1]);
                     }
                 }
             }
-            // logits in log2 plus V's exponent; d = 2^-e, vm = V's scale * d
+            // logits in log2 plus V's exponent, less the reference; d = 2^-e, vm = V's scale * d
             float d[KT][2], vm[KT][2];
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
@@ -537,7 +583,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
-                            z[t][nt][2 * y + x] = fmaf(z[t][nt][2 * y + x], ks[y] * qfac[nt][x], (float)e);
+                            z[t][nt][2 * y + x] = fmaf(z[t][nt][2 * y + x], ks[y] * qfac[nt][x], (float)e - m_run[nt][x]);
                 }
                 if (valid[t] != (IDX ? 0xffff : 16)) {
                     const bool v0 = IDX ? valid[t] >> g & 1 : g < valid[t], v1 = IDX ? valid[t] >> (g + 8) & 1 : g + 8 < valid[t];
@@ -548,7 +594,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                             if (!v0) z[t][nt][x] = -INFINITY;
                             if (!v1) z[t][nt][2 + x] = -INFINITY;
                         }
-                    if (!v0) d[t][0] = 0.f, vm[t][0] = 0.f;  // whatever an uncopied stage holds
+                    if (!v0) d[t][0] = 0.f, vm[t][0] = 0.f;  // whatever an uncopied scale holds
                     if (!v1) d[t][1] = 0.f, vm[t][1] = 0.f;
                 }
             }
@@ -563,18 +609,19 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                     for (int t = 1; t < KT; ++t) mx[x] = fmaxf(mx[x], fmaxf(z[t][nt][x], z[t][nt][2 + x]));
                 }
                 // the reference moves only when a logit exceeds it by more than 2^8
-                if (__any_sync(0xffffffffu, mx[0] > m_run[nt][0] + 8.f || mx[1] > m_run[nt][1] + 8.f)) {
-                    float alpha[2] = {1.f, 1.f};
+                if (!started || __any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > 8.f)) {
+                    float alpha[2];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 4));
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 8));
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 16));
-                        if (mx[x] > m_run[nt][x] + 8.f) {
-                            alpha[x] = ex2_approx(m_run[nt][x] - mx[x]);
-                            m_run[nt][x] = mx[x];
-                        }
+                        const float up = !started || mx[x] > 8.f ? fmaxf(mx[x], kPagedNone) : 0.f;
+                        alpha[x] = started ? ex2_approx(-up) : 1.f;  // at the start there is nothing to scale
+                        m_run[nt][x] += up;
                         l_run[nt][x] *= alpha[x];
+#pragma unroll
+                        for (int t = 0; t < KT; ++t) z[t][nt][x] -= up, z[t][nt][2 + x] -= up;
                     }
 #pragma unroll
                     for (int dt = 0; dt < 8; ++dt) {
@@ -588,7 +635,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                 for (int t = 0; t < KT; ++t) {
                     float p[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) p[x] = ex2_approx(z[t][nt][x] - m_run[nt][x & 1]);
+                    for (int x = 0; x < 4; ++x) p[x] = ex2_approx(z[t][nt][x]);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) l_run[nt][x] = fmaf(p[2 + x], d[t][1], fmaf(p[x], d[t][0], l_run[nt][x]));
                     // P^T (keys x heads) -> B operand (keys as K, heads as N)
@@ -596,33 +643,27 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                     pb[t][nt][1] = movmatrix_trans(pack_f16x2(p[2] * vm[t][1], p[3] * vm[t][1]));
                 }
             }
-            // O^T += V^T P^T: fragment dt's rows are dims 16 g + 2 dt and 16 g + 2 dt + 1
+            started = true;
+            // O^T += V^T P^T: fragment dt's rows are dims 16 dt + g and 16 dt + g + 8; its columns the tile's keys 2 j,
+            // 2 j + 1, 2 j + 8, 2 j + 9
+            static_assert(KT == 2, "a transposed load takes the step's two tiles");
 #pragma unroll
-            for (int t = 0; t < KT; ++t) {
-                if (!valid[t]) continue;  // nothing copied
-                const uint8_t* p = stage + t * 4096 + 2048 + 2 * j * kKvD + ((g ^ (2 * j)) << 4);
-                const uint4 A = *reinterpret_cast<const uint4*>(p), B = *reinterpret_cast<const uint4*>(p + kKvD);
-                const uint4 E = *reinterpret_cast<const uint4*>(p + 8 * kKvD), F = *reinterpret_cast<const uint4*>(p + 9 * kKvD);
-                const uint32_t aw[4] = {A.x, A.y, A.z, A.w}, bw[4] = {B.x, B.y, B.z, B.w};
-                const uint32_t ew[4] = {E.x, E.y, E.z, E.w}, fw[4] = {F.x, F.y, F.z, F.w};
+            for (int dt = 0; dt < 8; ++dt) {
+                uint32_t w[4];
+                ldmatrix_b8_x2_trans(w, smem_u32(stage) + v_row + ((dt ^ v_swz) << 4));
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
+                for (int t = 0; t < KT; ++t) {
+                    uint32_t a[4];
+                    kv_f16x4<FMT>(w[2 * t], a[0], a[2]);
+                    kv_f16x4<FMT>(w[2 * t + 1], a[1], a[3]);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t x = __byte_perm(aw[w], bw[w], half ? 0x7362 : 0x5140);
-                        const uint32_t y = __byte_perm(ew[w], fw[w], half ? 0x7362 : 0x5140);
-                        uint32_t a[4];
-                        kv_f16x4<FMT>(x, a[0], a[1]);
-                        kv_f16x4<FMT>(y, a[2], a[3]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma_16816_f16(o[nt][2 * w + half], a, pb[t][nt][0], pb[t][nt][1]);
-                    }
+                    for (int nt = 0; nt < NT; ++nt) mma_16816_f16(o[nt][dt], a, pb[t][nt][0], pb[t][nt][1]);
                 }
             }
         }
         used = st;
         st = st + 1 == S ? 0 : st + 1;
-        ++at;
+        ++now;
         if (--left) continue;
 
         // ---- the row's last tile in this block: the warps of a KV head exchange their outputs through the
@@ -639,8 +680,8 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                 [&](int p) { return src[p * HKV * (S * C::STAGE / 16)]; });
         }
         if (CLU) break;
-        at += kPagedRowTiles;
-        if (at >= w1) break;
+        now += kPagedRowTiles;
+        if (now >= units) break;
         int b, n;
         do paged_row(P, ++row, b, n);
         while (paged_count(P, n) == 0);
@@ -648,7 +689,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         begin_row(0, n);
         __syncthreads();  // the stages are read: the next copies may take them
     }
-    if (CLU && P.cluster == 1 && w1 == 0) {  // a row without keys
+    if (CLU && P.cluster == 1 && units == 0) {  // a row without keys
         uint4* o = reinterpret_cast<uint4*>(P.out + (long long)row0 * P.Hq * kKvD);
         for (int i = threadIdx.x; i < P.Hq * kKvD / 8; i += C::THREADS) o[i] = make_uint4(0, 0, 0, 0);
         if (P.lse)

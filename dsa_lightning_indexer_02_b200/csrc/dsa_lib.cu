@@ -508,18 +508,23 @@ dsa_status run_rope(const void* x, int dtype, int64_t T, int H, int D, RopeParam
 bool page_supported(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 int log2_of(int x) { return 31 - __builtin_clz((unsigned)x); }
 
-template <int FMT, bool INTER>
+template <int FMT, bool INTER, int PASSES>
 dsa_status launch_append_t(AppendParams P, int64_t units, cudaStream_t s) {
-    auto kern = kv_append_kernel<FMT, INTER>;
+    auto kern = kv_append_kernel<FMT, INTER, PASSES>;
     static DeviceFlags attr_set;
     if (!set_smem_limit(kern, 128 * (kKvD / 2) * 8, attr_set)) return DSA_ERR_CUDA;
     const int tokens = P.cu_new ? 1 << P.page_shift : 1;  // most tokens of a block
     const int heads = std::min(P.Hkv, kAppendRows / tokens);
     P.hg_shift = log2_of(heads);
-    const int threads = std::max(64, tokens * heads * kKvUnits / kAppendPasses);
+    const int threads = std::max(64, tokens * heads * kKvUnits / PASSES);
     LaunchScope ls(K_KV_APPEND, s);
     kern<<<dim3((unsigned)units, 2 * P.Hkv / heads), threads, tokens * P.n * 8, s>>>(P);
     return launch_status();
+}
+
+template <int FMT, bool INTER>
+dsa_status launch_append(const AppendParams& P, int64_t units, cudaStream_t s) {
+    return P.cu_new ? launch_append_t<FMT, INTER, kAppendPasses>(P, units, s) : launch_append_t<FMT, INTER, 1>(P, units, s);
 }
 
 // Workspace: two partials for each block that shares rows, then the rows' first tiles.
@@ -588,19 +593,19 @@ dsa_status launch_paged_t(PagedParams P, cudaStream_t s) {
     const int sms = num_sms();
     if (sms <= 0) return DSA_ERR_CUDA;
     constexpr int TK = C::NW / HKV * C::KT * 16;
-    // Blocks of a row, in tiles of time: a cluster of c takes ceil(tiles / c) of them for as many rows at once
-    // as clusters fit; dealing by units takes the even share, and for its second kernel (4 us) as long as
-    // kJoinTiles.  Rows count with the most keys they can have.
+    // Blocks of a row, in tiles of time (1.2 us each): a cluster of c takes ceil(tiles / c) of them for as many rows
+    // at once as clusters fit, and two more to join through shared memory; dealing by units takes the even share,
+    // and five for its second kernel.  Rows count with the most keys they can have.
     const int64_t most = std::min<int64_t>((int64_t)P.max_pages << P.page_shift, P.idx ? P.topk : INT32_MAX);
     const int64_t tiles = (most + TK - 1) / TK;
     const int ctas = std::min(C::CTAS * sms, kPagedPartCtas);
-    constexpr int kJoinTiles = 5;
+    constexpr int kJoinTiles = 5, kClusterTiles = 2;
     int64_t best = P.T <= kPagedSharedRows ? ((int64_t)P.T * (tiles + kPagedRowTiles) + ctas - 1) / ctas + kJoinTiles : INT64_MAX;
     P.cluster = P.T <= kPagedSharedRows ? 0 : 1;
     for (int c = 1; c <= 8; c *= 2) {
         const int fit = c == 1 ? C::CTAS * sms : paged_clusters<FMT, NT, HKV, IDX>(c, s);
         if (fit <= 0) continue;
-        const int64_t t = (P.T + fit - 1) / fit * ((tiles + c - 1) / c) + (c > 1);
+        const int64_t t = (P.T + fit - 1) / fit * ((tiles + c - 1) / c) + (c > 1 ? kClusterTiles : 0);
         if (t < best) best = t, P.cluster = c;
     }
     {
@@ -1202,8 +1207,8 @@ dsa_status dsa_kv_append(const void* k_new, const void* v_new, int64_t k_ts, int
     const int64_t units = cu_new ? (N >> P.page_shift) + 2 * (int64_t)B : B;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (kv_format == DSA_KV_E4M3)
-        return inter ? launch_append_t<KV_E4M3, true>(P, units, s) : launch_append_t<KV_E4M3, false>(P, units, s);
-    return inter ? launch_append_t<KV_INT8, true>(P, units, s) : launch_append_t<KV_INT8, false>(P, units, s);
+        return inter ? launch_append<KV_E4M3, true>(P, units, s) : launch_append<KV_E4M3, false>(P, units, s);
+    return inter ? launch_append<KV_INT8, true>(P, units, s) : launch_append<KV_INT8, false>(P, units, s);
 }
 
 dsa_status dsa_paged_attn(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,

@@ -29,7 +29,7 @@ namespace dsa {
 constexpr int kKvD = 128;
 constexpr int kKvEMin = -64;       // least scale exponent (an all-zero block gets it)
 constexpr int kKvUnits = 8;        // 16-dim units of a row (a token and head)
-constexpr int kAppendPasses = 4;   // most units of a thread
+constexpr int kAppendPasses = 4;   // most units of a thread (1 where every sequence has one token)
 constexpr int kAppendRows = 128;   // most rows of a block
 
 enum { KV_E4M3 = 0, KV_INT8 = 1 };
@@ -167,7 +167,16 @@ __device__ __forceinline__ float round_odd(double y) {
     return static_cast<double>(r) == y || !(y == y) ? r : __uint_as_float(__float_as_uint(r) | 1u);
 }
 
-template <int FMT, bool INTER>
+// The bytes of a pair turned by ph / 2^64 turns, in fp64.  Out of line: rarely taken, and long.
+template <int FMT>
+__device__ __noinline__ uint32_t kv_turn_exact(float e0, float e1, unsigned long long ph, float mscale, float inv) {
+    double s, c;
+    sincospi(static_cast<double>(static_cast<long long>(ph)) * 1.0842021724855044e-19, &s, &c);  // 2^-63
+    const double a = e0, b = e1, m = mscale;
+    return kv_round4<FMT>(round_odd(m * (a * c - b * s)) * inv, round_odd(m * (a * s + b * c)) * inv, 0.f, 0.f);
+}
+
+template <int FMT, bool INTER, int PASSES>
 __global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams P) {
     // cos, sin times mscale (K blocks), [tokens][4][n / 8][2]: pairs 2 k, 2 k + 1 of unit u at [k][u], so that the
     // units' 16-byte reads lie side by side
@@ -204,9 +213,9 @@ __global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams P)
                              (long long)h0 * (is_k ? P.k_hs : P.v_hs);
     const long long ts = is_k ? P.k_ts : P.v_ts, hs = is_k ? P.k_hs : P.v_hs;
     const int my_h = row0 & hmask;  // the same for all rows of this thread
-    uint4 ra[kAppendPasses], rb[kAppendPasses];
+    uint4 ra[PASSES], rb[PASSES];
 #pragma unroll
-    for (int i = 0; i < kAppendPasses; ++i) {
+    for (int i = 0; i < PASSES; ++i) {
         const int r = row0 + i * step;
         if (r < rows) {
             const __nv_bfloat16* at = in + (long long)(r >> hshift) * ts + my_h * hs;
@@ -241,12 +250,12 @@ __global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams P)
 
     // the largest finite magnitude of this thread's rows, which are of one head.  Turned keys stay in fp32 from
     // here on (f[0..8) of vector a, f[8..16) of vector b); values, and keys stored as they come, in bf16.
-    float f[kAppendPasses][16];
+    float f[PASSES][16];
     float m = 0.f;
     bool nan = false;
     if (n) {
 #pragma unroll
-        for (int i = 0; i < kAppendPasses; ++i) {
+        for (int i = 0; i < PASSES; ++i) {
             if (row0 + i * step >= rows) break;
             float p[8], q[8];
             RopeElem<__nv_bfloat16>::unpack(ra[i], p);
@@ -274,7 +283,7 @@ __global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams P)
     } else {
         __nv_bfloat162 most = __float2bfloat162_rn(0.f), seen = most;
 #pragma unroll
-        for (int i = 0; i < kAppendPasses; ++i) {
+        for (int i = 0; i < PASSES; ++i) {
             if (row0 + i * step >= rows) break;
             const uint32_t w[8] = {ra[i].x, ra[i].y, ra[i].z, ra[i].w, rb[i].x, rb[i].y, rb[i].z, rb[i].w};
 #pragma unroll
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams P)
         if (m == INFINITY) {
             m = 0.f;
 #pragma unroll
-            for (int i = 0; i < kAppendPasses; ++i) {
+            for (int i = 0; i < PASSES; ++i) {
                 if (row0 + i * step >= rows) break;
                 float v[16];
                 RopeElem<__nv_bfloat16>::unpack(ra[i], *reinterpret_cast<float(*)[8]>(v));
@@ -315,7 +324,7 @@ __global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams P)
     const float s = s_new[my_h], inv = 1.f / s;  // powers of two
     uint8_t* to = pages + (long long)slot0 * P.Hkv * kKvD + (h0 + my_h) * kKvD;
 #pragma unroll
-    for (int i = 0; i < kAppendPasses; ++i) {
+    for (int i = 0; i < PASSES; ++i) {
         const int r = row0 + i * step;
         if (r >= rows) break;
         uint32_t w[4];
@@ -364,13 +373,9 @@ __global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams P)
                     const int y = __ffs(todo) - 1;
                     const int lo = INTER ? 2 * y : y, hi = INTER ? 2 * y + 1 : 8 + y;
                     const unsigned at_lo = 255u << (8 * (lo & 3)), at_hi = 255u << (8 * (hi & 3));
-                    double sd, cd;
-                    const unsigned long long ph = p * rope_turn(P.inv_freq[u * 8 + y]);
-                    sincospi(static_cast<double>(static_cast<long long>(ph)) * 1.0842021724855044e-19, &sd, &cd);  // 2^-63
-                    const double e0 = __bfloat162float(at[lo < 8 ? a + lo : b + lo - 8]);
-                    const double e1 = __bfloat162float(at[hi < 8 ? a + hi : b + hi - 8]);
-                    const float y0 = round_odd(P.mscale * (e0 * cd - e1 * sd)), y1 = round_odd(P.mscale * (e0 * sd + e1 * cd));
-                    const uint32_t both = kv_round4<FMT>(y0 * inv, y1 * inv, 0.f, 0.f);
+                    const uint32_t both = kv_turn_exact<FMT>(__bfloat162float(at[lo < 8 ? a + lo : b + lo - 8]),
+                                                             __bfloat162float(at[hi < 8 ? a + hi : b + hi - 8]),
+                                                             p * rope_turn(P.inv_freq[u * 8 + y]), P.mscale, inv);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         if (lo >> 2 == k) w[k] = (w[k] & ~at_lo) | ((both & 255u) << (8 * (lo & 3)));

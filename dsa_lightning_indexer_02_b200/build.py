@@ -19,7 +19,7 @@ MARSHAL_SRC = os.path.join(HERE, "csrc", "marshal.cpp")
 MARSHAL = os.path.join(HERE, "_marshal.so")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v", "--expt-relaxed-constexpr", "-split-compile=0"]
+              "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v", "--expt-relaxed-constexpr"]
 
 
 def nvcc() -> str:

@@ -593,19 +593,23 @@ dsa_status launch_paged_t(PagedParams P, cudaStream_t s) {
     const int sms = num_sms();
     if (sms <= 0) return DSA_ERR_CUDA;
     constexpr int TK = C::NW / HKV * C::KT * 16;
-    // Blocks of a row, in tiles of time (1.2 us each): a cluster of c takes ceil(tiles / c) of them for as many rows
-    // at once as clusters fit, and two more to join through shared memory; dealing by units takes the even share,
-    // and five for its second kernel.  Rows count with the most keys they can have.
+    // How rows are spread, by times in tenths of a tile's (1.5 us), fitted to 1 to 128 rows of 60 to 8000 keys:
+    //   a cluster of c blocks a row  30 to start, 10 a tile, 12 to join through shared memory where c > 1; as many
+    //                                rows at once as clusters fit
+    //   rows dealt by units          70 with the joining kernel, 11.5 a unit of the even share
+    // (16 rows of 800 keys: dealt 12.9 us, clusters of 4 11.0; 16 of 8000: 34 and 40; 64 of 800: 19.4 and, of 2, 14.8;
+    // 128 of 200: 12.8 and, of 1, 9.4.)  Rows count with the most keys they can have, which suits dealing: so a
+    // dense row's tiles count for 13 in a cluster, whose longest row is waited for.
     const int64_t most = std::min<int64_t>((int64_t)P.max_pages << P.page_shift, P.idx ? P.topk : INT32_MAX);
     const int64_t tiles = (most + TK - 1) / TK;
     const int ctas = std::min(C::CTAS * sms, kPagedPartCtas);
-    constexpr int kJoinTiles = 5, kClusterTiles = 2;
-    int64_t best = P.T <= kPagedSharedRows ? ((int64_t)P.T * (tiles + kPagedRowTiles) + ctas - 1) / ctas + kJoinTiles : INT64_MAX;
-    P.cluster = P.T <= kPagedSharedRows ? 0 : 1;
+    int64_t best = INT64_MAX;
+    P.cluster = 1;
+    if (P.T <= kPagedSharedRows) best = 70 + ((int64_t)P.T * (tiles + kPagedRowTiles) + ctas - 1) / ctas * 23 / 2, P.cluster = 0;
     for (int c = 1; c <= 8; c *= 2) {
         const int fit = c == 1 ? C::CTAS * sms : paged_clusters<FMT, NT, HKV, IDX>(c, s);
         if (fit <= 0) continue;
-        const int64_t t = (P.T + fit - 1) / fit * ((tiles + c - 1) / c) + (c > 1 ? kClusterTiles : 0);
+        const int64_t t = (P.T + fit - 1) / fit * (30 + (tiles + c - 1) / c * (IDX ? 10 : 13) + (c > 1 ? 12 : 0));
         if (t < best) best = t, P.cluster = c;
     }
     {

@@ -36,7 +36,7 @@ namespace dsa {
 constexpr int kPagedPartCtas = 296;     // most blocks that share rows; each has two partial slots
 constexpr int kPagedSharedRows = 1184;  // most rows that are dealt by units
 constexpr int kPagedPartStride = kKvD + 4;  // floats of a partial: O[128], max, sum, 2 pad
-constexpr int kPagedRowTiles = 1;       // what the end of a row costs a block, in tiles, when rows are dealt
+constexpr int kPagedRowTiles = 2;       // what the end of a row costs a block, in tiles, when rows are dealt
 
 struct PagedParams {
     const __nv_bfloat16* q;            // [T, Hq, 128]

@@ -532,7 +532,7 @@ size_t paged_part_bytes(int Hq) { return align_up((size_t)2 * kPagedPartCtas * H
 size_t paged_ws_bytes(int Hq) { return paged_part_bytes(Hq) + align_up((size_t)(kPagedSharedRows + 1) * 8, 256); }
 
 template <int WPH>
-cudaError_t launch_combine_t(const PagedParams& P, int TK, cudaStream_t s) {
+void launch_combine_t(const PagedParams& P, int TK, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(P.T, std::max(1, std::min((P.Hq + 8 / WPH - 1) / (8 / WPH), 1184 / P.T)));
     cfg.blockDim = dim3(kCombineThreads);
@@ -542,7 +542,7 @@ cudaError_t launch_combine_t(const PagedParams& P, int TK, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_combine_kernel<WPH>, P, TK);
+    (void)cudaLaunchKernelEx(&cfg, paged_combine_kernel<WPH>, P, TK);  // its status is the last error too
 }
 
 template <int NT>
@@ -619,7 +619,7 @@ dsa_status launch_paged_t(PagedParams P, cudaStream_t s) {
         } else {
             cudaLaunchAttribute attr[1];
             const cudaLaunchConfig_t cfg = paged_config<NT>((int64_t)P.T * P.cluster, P.cluster, attr, s);
-            if (cudaLaunchKernelEx(&cfg, clustered, P) != cudaSuccess) return DSA_ERR_CUDA;
+            (void)cudaLaunchKernelEx(&cfg, clustered, P);  // its status is the last error too
         }
         const dsa_status st = launch_status();
         if (st != DSA_OK || P.cluster) return st;
@@ -627,10 +627,11 @@ dsa_status launch_paged_t(PagedParams P, cudaStream_t s) {
     // 8 warps on a head while there are few (row, head) pairs, down to one
     LaunchScope ls(K_COMBINE, s);
     const int pairs = P.T * P.Hq;
-    const cudaError_t e = pairs <= 1184 ? launch_combine_t<8>(P, TK, s)
-                          : pairs <= 2368 ? launch_combine_t<4>(P, TK, s)
-                          : pairs <= 4736 ? launch_combine_t<2>(P, TK, s) : launch_combine_t<1>(P, TK, s);
-    return e == cudaSuccess ? launch_status() : DSA_ERR_CUDA;
+    if (pairs <= 1184) launch_combine_t<8>(P, TK, s);
+    else if (pairs <= 2368) launch_combine_t<4>(P, TK, s);
+    else if (pairs <= 4736) launch_combine_t<2>(P, TK, s);
+    else launch_combine_t<1>(P, TK, s);
+    return launch_status();
 }
 
 template <int FMT, int NT>

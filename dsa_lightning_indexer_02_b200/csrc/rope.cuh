@@ -61,7 +61,7 @@ __device__ __forceinline__ void rope_sincos(uint32_t phase, float& c, float& s) 
 }
 
 // The same by the hardware's sine and cosine, whose absolute error on [-pi, pi] stays below 2^-21: for
-// results that are rounded to bf16 (half a step is 2^-9 of the value's size).
+// results that are rounded to bf16 (half a step is 2^-9 of the value at least).
 __device__ __forceinline__ void rope_sincos_fast(uint32_t phase, float& c, float& s) {
     __sincosf(static_cast<float>(static_cast<int>(phase)) * 1.4629180792671596e-9f, &s, &c);  // pi / 2^31
 }

@@ -600,3 +600,47 @@ def test_other_stream(cuda_ok):
     s.synchronize()
     ok()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("rows,most", [(1, 64), (3, 200), (16, 800), (40, 800), (64, 800), (128, 200), (160, 640),
+                                       (1, 4096), (5, 20000), (1184, 640), (1185, 64)])
+def test_attn_every_spread_of_rows(cuda_ok, rows, most):
+    """Row counts and table widths on both sides of each choice between dealt rows, clusters and one block a row;
+    rows from none to all of the keys the table can hold."""
+    cache = filled([most], 16, 4, E4M3, seed=rows)
+    rng = np.random.RandomState(rows)
+    n = rng.randint(0, most + 1, rows)
+    n[rng.randint(0, rows, 2)] = [0, most]
+    check_attn(cache, randn(6, rows, 8, 128), n, seq=[0] * rows)
+
+
+def test_graph_of_dealt_rows_and_two_calls_at_once(cuda_ok):
+    """Long rows shared by blocks and joined by a second kernel: captured and replayed for other lengths (none at
+    all among them), and called on two streams at once with a workspace each."""
+    cache = filled([9000, 5000, 20], 64, 2, INT8)
+    q = randn(0, 3, 16, 128).cuda()
+    out, lse = torch.full_like(q, 7.0), torch.zeros((3, 16), device="cuda")
+    n = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ws = torch.empty(dsa.workspace_size(dsa.DSA_OP_PAGED_ATTN, 1, 3, 16, 1, 1), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dsa.dsa_paged_attn(q, cache.k, cache.v, cache.ks, cache.vs, cache.table_gpu, n, 0.1, out, lse=lse, ws=ws)
+    lengths = [[9000, 5000, 20], [0, 0, 0], [1, 0, 17], [8999, 1, 0], [0, 4999, 20]]
+    wants = [attend(cache, q, v, 0.1) for v in lengths]
+    for v, (want, wlse) in zip(lengths, wants):
+        n.copy_(torch.tensor(v, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wlse)
+    assert not wants[1][0].any() and torch.isinf(wants[1][1]).all()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for i in range(10):
+        for s, (one, many) in enumerate(((0, 3), (3, 0))):
+            with torch.cuda.stream(streams[s]):
+                got[s].append((one, attend(cache, q, lengths[one], 0.1)))
+                got[s].append((many, attend(cache, q, lengths[many], 0.1)))
+    torch.cuda.synchronize()
+    for which, (o, l) in got[0] + got[1]:
+        assert torch.equal(o, wants[which][0]) and torch.equal(l, wants[which][1])
+    ok()

@@ -562,14 +562,14 @@ cudaLaunchConfig_t paged_config(int64_t grid, int cluster, cudaLaunchAttribute* 
     return cfg;
 }
 
-// Clusters of `cluster` (2, 4 or 8) blocks of the attention kernel that fit on the device at once; 0 if the query
+// Clusters of `cluster` (2 to 8) blocks of the attention kernel that fit on the device at once; 0 if the query
 // fails.  Asked once per device, kernel and size.
 template <int FMT, int NT, int HKV, bool IDX>
 int paged_clusters(int cluster, cudaStream_t s) {
-    static std::atomic<int> cache[kMaxDevices][4];  // 0: not asked yet
-    const int dev = current_device(), k = log2_of(cluster);
+    static std::atomic<int> cache[kMaxDevices][kPagedMostCluster + 1];  // 0: not asked yet
+    const int dev = current_device();
     if (dev < 0) return 0;
-    int n = cache[dev][k].load(std::memory_order_relaxed);
+    int n = cache[dev][cluster].load(std::memory_order_relaxed);
     if (!n) {
         cudaLaunchAttribute attr[1];
         const cudaLaunchConfig_t cfg = paged_config<NT>(cluster, cluster, attr, s);
@@ -577,7 +577,7 @@ int paged_clusters(int cluster, cudaStream_t s) {
             (void)cudaGetLastError();
             n = -1;
         }
-        cache[dev][k].store(n, std::memory_order_relaxed);
+        cache[dev][cluster].store(n, std::memory_order_relaxed);
     }
     return n > 0 ? n : 0;
 }
@@ -598,15 +598,16 @@ dsa_status launch_paged_t(PagedParams P, cudaStream_t s) {
     //                                rows at once as clusters fit
     //   rows dealt by units          70 with the joining kernel, 11.5 a unit of the even share
     // (16 rows of 800 keys: dealt 12.9 us, clusters of 4 11.0; 16 of 8000: 34 and 40; 64 of 800: 19.4 and, of 2, 14.8;
-    // 128 of 200: 12.8 and, of 1, 9.4.)  Rows count with the most keys they can have, which suits dealing: so a
-    // dense row's tiles count for 13 in a cluster, whose longest row is waited for.
+    // 128 of 200: 12.8 and, of 1, 9.4; 16 of 2048 selected keys: clusters of 4 16.1, of 6 13.3.)  Rows count with
+    // the most keys they can have, which suits dealing: so a dense row's tiles count for 13 in a cluster, whose
+    // longest row is waited for.
     const int64_t most = std::min<int64_t>((int64_t)P.max_pages << P.page_shift, P.idx ? P.topk : INT32_MAX);
     const int64_t tiles = (most + TK - 1) / TK;
     const int ctas = std::min(C::CTAS * sms, kPagedPartCtas);
     int64_t best = INT64_MAX;
     P.cluster = 1;
     if (P.T <= kPagedSharedRows) best = 70 + ((int64_t)P.T * (tiles + kPagedRowTiles) + ctas - 1) / ctas * 23 / 2, P.cluster = 0;
-    for (int c = 1; c <= 8; c *= 2) {
+    for (int c = 1; c <= kPagedMostCluster; ++c) {
         const int fit = c == 1 ? C::CTAS * sms : paged_clusters<FMT, NT, HKV, IDX>(c, s);
         if (fit <= 0) continue;
         const int64_t t = (P.T + fit - 1) / fit * (30 + (tiles + c - 1) / c * (IDX ? 10 : 13) + (c > 1 ? 12 : 0));

@@ -23,7 +23,7 @@
 //     one block holds whole is finished there; of the others each block writes its unnormalised part, and
 //     paged_combine_kernel joins them.
 //   - Where that second kernel would cost more than even shares save (few keys, or rows enough to fill the
-//     GPU), a row gets a cluster of 1, 2, 4 or 8 blocks, which split its tiles evenly and join their outputs
+//     GPU), a row gets a cluster of 1 to 8 blocks, which split its tiles evenly and join their outputs
 //     through each other's shared memory.
 //
 // Measured (32 query heads):
@@ -32,8 +32,8 @@
 //                                        KV head; issue slots 55 % busy with 3 warps a scheduler)
 //   1024 rows x 2048 of 32768 keys       253 us, 8.5 TB/s of gathered rows, from L2: the same (57 %, 590 instructions
 //                                        for a warp's 32 keys; leaving out V's conversions alone saves 3 %)
-//   16 rows x 2048 of 131328 keys        16.0 us (5.3 for the bytes): latency of launch, look-up, three tiles, join
-//   1 row of 777 keys                    9.3 us: latency of launch, look-up, two tiles, join
+//   16 rows x 2048 of 131328 keys        13.3 us (5.3 for the bytes): latency of launch, look-up, four tiles, join
+//   1 row of 777 keys                    9.2 us: latency of launch, look-up, two tiles, join
 #pragma once
 
 #include <type_traits>
@@ -44,6 +44,7 @@ namespace dsa {
 
 constexpr int kPagedPartCtas = 296;     // most blocks that share rows; each has two partial slots
 constexpr int kPagedSharedRows = 1184;  // most rows that are dealt by units
+constexpr int kPagedMostCluster = 8;    // most blocks of a cluster (the most that any device takes)
 constexpr int kPagedPartStride = kKvD + 4;  // floats of a partial: O[128], max, sum, 2 pad
 constexpr int kPagedRowTiles = 2;       // what the end of a row costs a block, in tiles, when rows are dealt
 
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
             const uint32_t ml = smem_u32(reinterpret_cast<const float4*>(xch) + head * (NT * 4) + (i >> 3) * 4 + j);
             const uint32_t src = smem_u32(reinterpret_cast<const float4*>(smem + head * (S * C::STAGE)) + i * 32 + lane);
             join(
-                std::integral_constant<int, 8>(), i >> 3, i & 7, P.cluster, [&](int p) { return ld_cluster(cluster_addr(ml, p)); },
+                std::integral_constant<int, kPagedMostCluster>(), i >> 3, i & 7, P.cluster, [&](int p) { return ld_cluster(cluster_addr(ml, p)); },
                 [&](int p) { return ld_cluster(cluster_addr(src, p)); });
         }
         cluster_sync();  // no block leaves while another reads its shared memory

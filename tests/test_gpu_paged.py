@@ -603,7 +603,7 @@ def test_other_stream(cuda_ok):
 
 
 @pytest.mark.parametrize("rows,most", [(1, 64), (3, 200), (16, 800), (40, 800), (64, 800), (128, 200), (160, 640),
-                                       (1, 4096), (5, 20000), (1184, 640), (1185, 64)])
+                                       (1, 4096), (5, 20000), (1184, 640), (1185, 64), (1, 288), (2, 480), (3, 576), (1, 672)])
 def test_attn_every_spread_of_rows(cuda_ok, rows, most):
     """Row counts and table widths on both sides of each choice between dealt rows, clusters and one block a row;
     rows from none to all of the keys the table can hold."""

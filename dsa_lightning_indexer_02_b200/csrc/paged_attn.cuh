@@ -33,7 +33,7 @@
 //   1024 rows x 2048 of 32768 keys       253 us, 8.5 TB/s of gathered rows, from L2: the same (57 %, 590 instructions
 //                                        for a warp's 32 keys; leaving out V's conversions alone saves 3 %)
 //   16 rows x 2048 of 131328 keys        13.3 us (5.3 for the bytes): latency of launch, look-up, four tiles, join
-//   1 row of 777 keys                    9.2 us: latency of launch, look-up, two tiles, join
+//   1 row of 777 keys                    8.9 us: latency of launch, look-up, two tiles, join
 #pragma once
 
 #include <type_traits>

@@ -509,22 +509,31 @@ bool page_supported(int page) { return page == 16 || page == 32 || page == 64 ||
 int log2_of(int x) { return 31 - __builtin_clz((unsigned)x); }
 
 template <int FMT, bool INTER, int PASSES>
-dsa_status launch_append_t(AppendParams P, int64_t units, cudaStream_t s) {
+dsa_status launch_append_t(AppendParams P, int64_t units, int rows, cudaStream_t s) {
     auto kern = kv_append_kernel<FMT, INTER, PASSES>;
     static DeviceFlags attr_set;
     if (!set_smem_limit(kern, 128 * (kKvD / 2) * 8, attr_set)) return DSA_ERR_CUDA;
-    const int tokens = P.cu_new ? 1 << P.page_shift : 1;  // most tokens of a block
-    const int heads = std::min(P.Hkv, kAppendRows / tokens);
-    P.hg_shift = log2_of(heads);
-    const int threads = std::max(64, tokens * heads * kKvUnits / PASSES);
+    const int tokens = P.cu_new ? 1 << P.page_shift : 1, threads = std::max(64, rows * kKvUnits / PASSES);
     LaunchScope ls(K_KV_APPEND, s);
-    kern<<<dim3((unsigned)units, 2 * P.Hkv / heads), threads, tokens * P.n * 8, s>>>(P);
+    kern<<<dim3((unsigned)units, 2 * P.Hkv >> P.hg_shift), threads, tokens * P.n * 8, s>>>(P);
     return launch_status();
 }
 
+// One unit a thread where every sequence has one token.  Otherwise four, which leave more blocks on an SM; or two
+// while that makes no more than 1024 threads an SM, where a block's own time counts (8 sequences of up to 500
+// tokens, 4 KV heads, pages of 64: 7.5 us with four, 6.8 with two; 16 of 1000: 9.3 and 10.9); no more than 512 where
+// no sines are made (the same 8 sequences: 5.4 and 6.5; of up to 100 tokens: 4.0 and 3.7).
 template <int FMT, bool INTER>
-dsa_status launch_append(const AppendParams& P, int64_t units, cudaStream_t s) {
-    return P.cu_new ? launch_append_t<FMT, INTER, kAppendPasses>(P, units, s) : launch_append_t<FMT, INTER, 1>(P, units, s);
+dsa_status launch_append(AppendParams P, int64_t units, cudaStream_t s) {
+    const int tokens = P.cu_new ? 1 << P.page_shift : 1;  // most tokens of a block
+    const int heads = std::min(P.Hkv, kAppendRows / tokens), rows = tokens * heads;
+    P.hg_shift = log2_of(heads);
+    if (!P.cu_new) return launch_append_t<FMT, INTER, 1>(P, units, rows, s);
+    const int sms = num_sms();
+    if (sms <= 0) return DSA_ERR_CUDA;
+    if (units * (2 * P.Hkv / heads) * (rows * kKvUnits / 2) <= (P.n ? 1024ll : 512ll) * sms)
+        return launch_append_t<FMT, INTER, 2>(P, units, rows, s);
+    return launch_append_t<FMT, INTER, 4>(P, units, rows, s);
 }
 
 // Workspace: two partials for each block that shares rows, then the rows' first tiles.

@@ -10,7 +10,7 @@
 // unscaled, in fp16.
 //
 // Append: one block per touched page (of up to 128 rows of a token and head) for K and one for V.  A thread
-// owns 16 dims of four rows at most, both members of the pairs that it turns; they stay in registers
+// owns 16 dims of one, two or four rows, both members of the pairs that it turns; they stay in registers
 // between finding each head's largest magnitude and rounding, so every input is read once and every byte
 // written once.  The sines and cosines are made once per (token, pair) in shared memory for all heads.
 //
@@ -18,10 +18,10 @@
 // values.  Where the interval of twice that error around a value rounds to two different bytes, the pair is
 // computed again in fp64, so the stored byte is the exact product's.
 //
-// Measured: 16 single tokens, 4 KV heads 4.6 us, a launch and two dependent loads more than an empty kernel's 2.2;
-// 23 K tokens of 8 sequences 23.8 us, where the bytes alone take 11: bound by instructions (issue slots 57 % busy, two
-// blocks of 256 threads an SM): by count of operations a third of a key block's make sines, which its two heads share,
-// and a fifth round twice.
+// Measured: 16 single tokens, 4 KV heads 4.5 us, a launch and two dependent loads more than an empty kernel's 2.2; 61
+// chunks of up to 37 tokens, int8 3.3 us; 23 K tokens of 8 sequences 23.5 us, where the bytes alone take 11: bound by
+// instructions (issue slots 57 % busy, two blocks of 256 threads an SM): by count of operations a third of a key
+// block's make sines, which its two heads share, and a fifth round twice.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -34,7 +34,6 @@ namespace dsa {
 constexpr int kKvD = 128;
 constexpr int kKvEMin = -64;       // least scale exponent (an all-zero block gets it)
 constexpr int kKvUnits = 8;        // 16-dim units of a row (a token and head)
-constexpr int kAppendPasses = 4;   // most units of a thread (1 where every sequence has one token)
 constexpr int kAppendRows = 128;   // most rows of a block
 
 enum { KV_E4M3 = 0, KV_INT8 = 1 };
@@ -181,8 +180,9 @@ __device__ __noinline__ uint32_t kv_turn_exact(float e0, float e1, unsigned long
     return kv_round4<FMT>(round_odd(m * (a * c - b * s)) * inv, round_odd(m * (a * s + b * c)) * inv, 0.f, 0.f);
 }
 
+// PASSES: units of a thread, 1, 2 or 4.
 template <int FMT, bool INTER, int PASSES>
-__global__ void __launch_bounds__(256, 2) kv_append_kernel(const AppendParams P) {
+__global__ void __launch_bounds__(PASSES == 2 ? 512 : 256, PASSES == 2 ? 1 : 2) kv_append_kernel(const AppendParams P) {
     // cos, sin times mscale (K blocks), [tokens][4][n / 8][2]: pairs 2 k, 2 k + 1 of unit u at [k][u], so that the
     // units' 16-byte reads lie side by side
     extern __shared__ __align__(16) float2 s_turn[];

@@ -201,6 +201,10 @@ APPEND = [
     (32, 2, INT8, [[31, 33, 0, 5], [1, 1, 1, 1], [64, 1, 7, 32]]),
     (128, 4, INT8, [[300, 1, 0], [1, 127, 128], [1, 1, 1]]),
     (128, 1, E4M3, [[5], [123], [1], [260]]),
+    # sequences enough that a thread takes four rows, not two
+    (64, 4, E4M3, [[i % 70 for i in range(150)], [i * 7 % 66 for i in range(150)]]),
+    (16, 2, INT8, [[i % 19 for i in range(700)], [i * 5 % 18 for i in range(700)]]),
+    (128, 1, E4M3, [[i * 3 % 131 for i in range(90)], [i % 60 for i in range(90)]]),
 ]
 
 

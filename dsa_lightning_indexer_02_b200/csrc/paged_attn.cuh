@@ -30,7 +30,7 @@
 //   16 x 131328 keys, 4 KV heads, e4m3   317-336 us, 6.3-6.7 TB/s, 98-104 % of the copy rate: bound by memory
 //   122 rows of 1 to 16000 keys, 2 KV heads, int8   74 us, 2.2 TB/s: bound by instructions and their latencies (16 heads a
 //                                        KV head; issue slots 55 % busy with 3 warps a scheduler)
-//   1024 rows x 2048 of 32768 keys       253 us, 8.5 TB/s of gathered rows, from L2: the same (57 %, 590 instructions
+//   1024 rows x 2048 of 32768 keys       253 us, 8.5 TB/s of gathered rows, from L2: the same (56 %, 560 instructions
 //                                        for a warp's 32 keys; leaving out V's conversions alone saves 3 %)
 //   16 rows x 2048 of 131328 keys        13.3 us (5.3 for the bytes): latency of launch, look-up, four tiles, join
 //   1 row of 777 keys                    8.9 us: latency of launch, look-up, two tiles, join

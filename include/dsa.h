@@ -296,9 +296,10 @@ dsa_status dsa_rope_freqs(int rot_dim, double theta, int scaling, double factor,
  *   ctx_len       int32 [B]: tokens already cached.  Token i of sequence b goes to position
  *                 ctx_len[b] + i.  ctx_len is not changed.
  *   page_table    int32 [B, max_pages]: position p lies in page page_table[b, p / page_size], slot
- *                 p mod page_size.  Only entries of touched pages are read.  A page belongs to
- *                 one sequence.
- *   k_pages, v_pages  [num_pages, page_size, Hkv, D] bytes, format DSA_KV_E4M3 or DSA_KV_INT8
+ *                 p mod page_size.  Only entries of touched pages are read.  A page that is written
+ *                 belongs to one sequence (pages that are only read later may be shared).
+ *   k_pages, v_pages  [num_pages, page_size, Hkv, D] bytes, format DSA_KV_E4M3 or DSA_KV_INT8; like the
+ *                 scales they must not overlap each other or the inputs
  *   k_scale, v_scale  fp32 [num_pages, Hkv]: a byte stands for scale * its e4m3 or int8 value
  *   rot_dim       0: keys are stored as they come.  Otherwise keys are turned as by dsa_rope
  *                 (inv_freq, rot_offset, layout, mscale) at position rope_pos[n], int32 [N], or
@@ -332,6 +333,7 @@ dsa_status dsa_kv_append(const void *k_new, const void *v_new, int64_t k_ts, int
  *               first min(topk, n_keys[t]) entries are read; entries < 0 or >= n_keys[t] are
  *               skipped, one that is repeated counts as often as it stands there.
  *   out         bf16 [T, Hq, D];  lse  fp32 [T, Hq] natural-log sum-exp, or NULL
+ * out, lse and ws must not overlap the inputs or one another.
  * A row without keys gets out = 0 and lse = -inf.  The cache, its scales and page_table as for
  * dsa_kv_append; any finite scales will do (those of dsa_kv_append are powers of two).  Only pages
  * that hold attended keys are read, and of those only attended tokens.

@@ -1161,12 +1161,12 @@ dsa_status dsa_rope_freqs(int rot_dim, double theta, int scaling, double factor,
     if (scaling == DSA_ROPE_NTK) base = theta * std::pow(factor, rot_dim / double(rot_dim - 2));
     if (scaling == DSA_ROPE_YARN) {
         // pair i turns orig_len * theta^(-i/n) / (2 pi) times over orig_len positions; the pairs that turn
-        // beta_fast and beta_slow times bound the ramp
+        // beta_fast and beta_slow times bound the ramp, whose end may lie behind the last pair
         const double two_pi = 6.283185307179586;
         lo = n * std::log(orig_len / (beta_fast * two_pi)) / std::log(theta);
         hi = n * std::log(orig_len / (beta_slow * two_pi)) / std::log(theta);
         lo = std::max(0.0, std::floor(lo));
-        hi = std::min(double(n - 1), std::ceil(hi));
+        hi = std::min(double(rot_dim - 1), std::ceil(hi));
         if (!(hi > lo)) hi = lo + 0.001;
     }
     for (int i = 0; i < n; ++i) {

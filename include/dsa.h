@@ -279,7 +279,9 @@ dsa_status dsa_rope(const void *x, int dtype, int64_t T, int H, int D, int64_t x
  *                    frequency is divided by factor, the fastest kept; mscale 1
  *   DSA_ROPE_YARN    pairs that turn more than beta_fast times over orig_len positions are kept,
  *                    those that turn less than beta_slow times are divided by factor, with a linear
- *                    ramp over the pair index between; mscale = 0.1 ln(factor) + 1 (factor > 1)
+ *                    ramp over the pair index between, from the last index kept to the first one
+ *                    divided, which may lie behind the last pair (rot_dim - 1 at most);
+ *                    mscale = 0.1 ln(factor) + 1 (factor > 1)
  * Errors: DSA_ERR_INVALID_ARG unless rot_dim is a positive even number, theta > 1, factor >= 1 (all but
  * PLAIN) and, for YARN, orig_len > 0 and beta_fast > beta_slow > 0; NTK needs rot_dim > 2.
  */

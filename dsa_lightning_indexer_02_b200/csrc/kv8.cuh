@@ -16,10 +16,13 @@
 //
 // Rounding of turned keys: fp32's own error moves one value in some 10^5 across a border between two 8-bit
 // values.  Where the interval of twice that error around a value rounds to two different bytes, the pair is
-// computed again in fp64, so the stored byte is the exact product's.
+// computed again in fp64, so the stored byte is the exact product's.  Where a head's largest lies within that error of
+// a border between two scales (one in some 2^18, but one in 128 where a slow pair leaves a bf16 value almost as it
+// was), the block settles the scale in fp64 when all else is done, and rounds that head's rows again if fp32 had it
+// wrong.  Done out of line, this costs a prefill 0.1 us of 23.5; decided before the rows are rounded, 1.9.
 //
-// Measured: 16 single tokens, 4 KV heads 4.5 us, a launch and two dependent loads more than an empty kernel's 2.2; 61
-// chunks of up to 37 tokens, int8 3.3 us; 23 K tokens of 8 sequences 23.5 us, where the bytes alone take 11: bound by
+// Measured: 16 single tokens, 4 KV heads 4.1 us, a launch and two dependent loads more than an empty kernel's 2.2; 61
+// chunks of up to 37 tokens, int8 3.4 us; 23 K tokens of 8 sequences 23.6 us, where the bytes alone take 11: bound by
 // instructions (issue slots 57 % busy, two blocks of 256 threads an SM): by count of operations a third of a key
 // block's make sines, which its two heads share, and a fifth round twice.
 #pragma once
@@ -62,6 +65,12 @@ __device__ __forceinline__ int kv_exponent(float amax) {
     const uint32_t most = FMT == KV_E4M3 ? 0x600000u : 0x7e0000u;
     const int e = x - (FMT == KV_E4M3 ? 8 : 6) + ((bits & 0x7fffffu) > most ? 1 : 0);
     return max(e, kKvEMin);
+}
+// Whether fp32's error may have put a largest turned magnitude on the wrong side of a border between two scales:
+// it is off by 2^-20.9 at most (where bytes are rounded, below), which is less than 16 steps next to a border.
+template <int FMT>
+__device__ __forceinline__ bool kv_near_border(uint32_t bits) {
+    return (bits & 0x7fffffu) - ((FMT == KV_E4M3 ? 0x600000u : 0x7e0000u) - 16u) <= 32u;
 }
 __device__ __forceinline__ float kv_pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
@@ -180,14 +189,85 @@ __device__ __noinline__ uint32_t kv_turn_exact(float e0, float e1, unsigned long
     return kv_round4<FMT>(round_odd(m * (a * c - b * s)) * inv, round_odd(m * (a * s + b * c)) * inv, 0.f, 0.f);
 }
 
+// What a block's threads share: per head the largest magnitude's bits, the page's scale before and after, and whether
+// an exact product lies above the border that the largest is next to.
+struct AppendShared {
+    unsigned amax[4];
+    float old[4], now[4];
+    int over[4];
+};
+
+// Settles the scales of heads whose largest magnitude is next to a border, once the rows are rounded: pairs long enough
+// to reach the border are turned in fp64, and a head's rows rounded again, every pair in fp64, where its scale changes.
+// All threads of a key block call it, each for its own rows (their first token is i0 at position p0); out of line, so
+// that the rows' registers are not kept for it.
+template <int FMT, bool INTER>
+__device__ __noinline__ void kv_settle_scale(const AppendParams& P, AppendShared& sh, const __nv_bfloat16* in, uint8_t* to, float* scale,
+                                             int a, int b, int i0, int p0, int rows) {
+    const int tid = threadIdx.x, u = tid & (kKvUnits - 1), row0 = tid / kKvUnits, step = blockDim.x / kKvUnits;
+    const int hshift = P.hg_shift, hmask = (1 << hshift) - 1, my_h = row0 & hmask;
+    const bool turned = u < P.n / 8;
+    const float most_of = FMT == KV_E4M3 ? 448.f : 127.f;
+    auto lower = [&](int h) { return kv_exponent<FMT>(__uint_as_float(sh.amax[h]) * (1.f - 1.9073486328125e-6f)); };  // 2^-19
+    // pair y of row r: where its members stand in the row, and its turn
+    auto pair = [&](int y, int& lo, int& hi) {
+        lo = INTER ? 2 * y : y, hi = INTER ? 2 * y + 1 : 8 + y;
+        lo = lo < 8 ? a + lo : b + lo - 8, hi = hi < 8 ? a + hi : b + hi - 8;
+    };
+    auto turn = [&](int r, int y) {
+        const int t = r >> hshift;
+        const long long pos = P.rope_pos ? (long long)P.rope_pos[i0 + t] : (long long)(p0 + t);
+        return static_cast<unsigned long long>(pos) * rope_turn(P.inv_freq[u * 8 + y]);
+    };
+    const float most = most_of * kv_pow2(lower(my_h));
+    if (turned && kv_near_border<FMT>(sh.amax[my_h])) {
+#pragma unroll 1
+        for (int r = row0; r < rows; r += step) {
+            const __nv_bfloat16* at = in + (long long)(r >> hshift) * P.k_ts + my_h * P.k_hs;
+#pragma unroll 1
+            for (int y = 0; y < 8; ++y) {
+                int lo, hi;
+                pair(y, lo, hi);
+                const float e0 = __bfloat162float(at[lo]), e1 = __bfloat162float(at[hi]);
+                if (!((e0 * e0 + e1 * e1) * (P.mscale * P.mscale) >= most * most * 0.9999f)) continue;  // a turn keeps its length
+                double sn, cs;
+                sincospi(static_cast<double>(static_cast<long long>(turn(r, y))) * 1.0842021724855044e-19, &sn, &cs);  // 2^-63
+                const double x0 = e0, x1 = e1, m = P.mscale;
+                const double y0 = fabs(m * (x0 * cs - x1 * sn)), y1 = fabs(m * (x0 * sn + x1 * cs));
+                if ((y0 > most && y0 < INFINITY) || (y1 > most && y1 < INFINITY)) sh.over[my_h] = 1;
+            }
+        }
+    }
+    const float before = sh.now[my_h];
+    __syncthreads();
+    if (tid <= hmask && kv_near_border<FMT>(sh.amax[tid]))
+        scale[tid] = sh.now[tid] = fmaxf(sh.old[tid], kv_pow2(max(lower(tid) + sh.over[tid], kKvEMin)));
+    __syncthreads();
+    const float now = sh.now[my_h];
+    if (now == before) return;
+#pragma unroll 1
+    for (int r = row0; r < rows; r += step) {
+        const __nv_bfloat16* at = in + (long long)(r >> hshift) * P.k_ts + my_h * P.k_hs;
+        uint8_t* dst = to + (long long)(r >> hshift) * P.Hkv * kKvD;
+#pragma unroll 1
+        for (int y = 0; y < 8; ++y) {
+            int lo, hi;
+            pair(y, lo, hi);
+            const float e0 = __bfloat162float(at[lo]), e1 = __bfloat162float(at[hi]);
+            const uint32_t both = turned ? kv_turn_exact<FMT>(e0, e1, turn(r, y), P.mscale, 1.f / now)
+                                         : kv_round4<FMT>(e0 / now, e1 / now, 0.f, 0.f);
+            dst[lo] = both & 255u, dst[hi] = both >> 8 & 255u;
+        }
+    }
+}
+
 // PASSES: units of a thread, 1, 2 or 4.
 template <int FMT, bool INTER, int PASSES>
-__global__ void __launch_bounds__(PASSES == 2 ? 512 : 256, PASSES == 2 ? 1 : 2) kv_append_kernel(const AppendParams P) {
+__global__ void __launch_bounds__(PASSES == 2 ? 512 : 256, PASSES == 2 ? 1 : 2) kv_append_kernel(const __grid_constant__ AppendParams P) {
     // cos, sin times mscale (K blocks), [tokens][4][n / 8][2]: pairs 2 k, 2 k + 1 of unit u at [k][u], so that the
     // units' 16-byte reads lie side by side
     extern __shared__ __align__(16) float2 s_turn[];
-    __shared__ unsigned s_amax[4];
-    __shared__ float s_old[4], s_new[4];
+    __shared__ __align__(16) AppendShared sh;
     const int tid = threadIdx.x, lane = tid & 31;
     const bool is_k = (blockIdx.y & 1) == 0;
     const int n = is_k ? P.n : 0, hshift = P.hg_shift, hmask = (1 << hshift) - 1, h0 = (blockIdx.y >> 1) << hshift;
@@ -247,9 +327,10 @@ __global__ void __launch_bounds__(PASSES == 2 ? 512 : 256, PASSES == 2 ? 1 : 2) 
     uint8_t* pages = (is_k ? P.k_pages : P.v_pages) + (long long)pid * page * P.Hkv * kKvD;
     float* scale = (is_k ? P.k_scale : P.v_scale) + (long long)pid * P.Hkv + h0;
     float old = 0.f;
-    if (tid <= hmask) {
-        s_amax[tid] = 0u;
-        old = slot0 ? scale[tid] : 0.f;  // consumed after the pass over the rows
+    if (tid < 4) {
+        sh.amax[tid] = 0u;
+        sh.over[tid] = 0;
+        if (tid <= hmask) old = slot0 ? scale[tid] : 0.f;  // consumed after the pass over the rows
     }
     __syncthreads();
 
@@ -314,19 +395,24 @@ __global__ void __launch_bounds__(PASSES == 2 ? 512 : 256, PASSES == 2 ? 1 : 2) 
     }
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (u == 0 && row0 < rows) atomicMax(&s_amax[my_h], __float_as_uint(m));  // m >= 0: bits keep the order
+    if (u == 0 && row0 < rows) atomicMax(&sh.amax[my_h], __float_as_uint(m));  // m >= 0: bits keep the order
     if (FMT == KV_INT8 && nan) record_error(DSA_DEV_ERR_BOUNDS, 0xa04);
     __syncthreads();
     if (tid <= hmask) {
-        const float s = fmaxf(old, kv_pow2(kv_exponent<FMT>(__uint_as_float(s_amax[tid]))));
-        s_old[tid] = old;
-        s_new[tid] = s;
+        const float s = fmaxf(old, kv_pow2(kv_exponent<FMT>(__uint_as_float(sh.amax[tid]))));
+        sh.old[tid] = old;
+        sh.now[tid] = s;
         scale[tid] = s;
+    }
+    bool open = false;  // the same in all threads
+    if (n) {
+        const uint4 top = *reinterpret_cast<const uint4*>(sh.amax);
+        open = kv_near_border<FMT>(top.x) || kv_near_border<FMT>(top.y) || kv_near_border<FMT>(top.z) || kv_near_border<FMT>(top.w);
     }
     __syncthreads();
 
     // round and store the new rows
-    const float s = s_new[my_h], inv = 1.f / s;  // powers of two
+    const float s = sh.now[my_h], inv = 1.f / s;  // powers of two
     uint8_t* to = pages + (long long)slot0 * P.Hkv * kKvD + (h0 + my_h) * kKvD;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
@@ -394,12 +480,14 @@ __global__ void __launch_bounds__(PASSES == 2 ? 512 : 256, PASSES == 2 ? 1 : 2) 
         *reinterpret_cast<uint2*>(dst + b) = make_uint2(w[2], w[3]);
     }
 
+    if (open) kv_settle_scale<FMT, INTER>(P, sh, in, to, scale, a, b, S.i0, S.p0, rows);
+
     // tokens that the page held before: rounded again where their head's scale grew
     if (!slot0) return;
     for (int e = tid; e < slot0 << (hshift + 3); e += blockDim.x) {
         const int h = (e >> 3) & hmask;
-        if (s_old[h] == s_new[h]) continue;
-        const float ratio = s_old[h] / s_new[h];
+        if (sh.old[h] == sh.now[h]) continue;
+        const float ratio = sh.old[h] / sh.now[h];
         uint4* at = reinterpret_cast<uint4*>(pages + ((long long)(e >> (hshift + 3)) * P.Hkv + h0 + h) * kKvD) + (e & 7);
         const uint4 v = *at;
         uint32_t w[4] = {v.x, v.y, v.z, v.w};

@@ -306,7 +306,7 @@ dsa_status dsa_rope_freqs(int rot_dim, double theta, int scaling, double factor,
  *   rot_dim       0: keys are stored as they come.  Otherwise keys are turned as by dsa_rope
  *                 (inv_freq, rot_offset, layout, mscale) at position rope_pos[n], int32 [N], or
  *                 where rope_pos is NULL at the cache position; the turned value is not rounded in
- *                 between.
+ *                 between.  |mscale| (|a| + |b|) of a pair has to stay within fp32's range.
  * A scale is the least power of two (2^-64 at least) with which the page's largest magnitude of
  * that head fits 448 (e4m3) or 127 (int8).  Writing slot 0 starts a page anew, whatever it held;
  * otherwise the page's scale never falls, and when it rises the tokens in the slots before the new

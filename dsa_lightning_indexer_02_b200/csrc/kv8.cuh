@@ -159,12 +159,13 @@ __device__ __forceinline__ AppendSpan append_span(const AppendParams& P, int uni
     return S;
 }
 
-// Largest of 16 magnitudes; infinities and NaN do not count.
-__device__ __forceinline__ float kv_amax(const float (&f)[16]) {
+// Largest of 16 magnitudes; infinities, which it tells of, and NaN do not count.
+__device__ __forceinline__ float kv_amax(const float (&f)[16], bool& infinite) {
     float m = 0.f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(f[j]));  // passes NaN over
-    if (m == INFINITY) {
+    infinite = m == INFINITY;
+    if (infinite) {
         m = 0.f;
 #pragma unroll
         for (int j = 0; j < 16; ++j)
@@ -339,6 +340,7 @@ __global__ void __launch_bounds__(PASSES == 2 ? 512 : 256, PASSES == 2 ? 1 : 2) 
     float f[PASSES][16];
     float m = 0.f;
     bool nan = false;
+    unsigned infinite = 0;  // bit i: turned row i has an infinity
     if (n) {
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
@@ -360,7 +362,9 @@ __global__ void __launch_bounds__(PASSES == 2 ? 512 : 256, PASSES == 2 ? 1 : 2) 
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[i][j] = p[j], f[i][8 + j] = q[j];
             }
-            m = fmaxf(m, kv_amax(f[i]));
+            bool inf;
+            m = fmaxf(m, kv_amax(f[i], inf));
+            if (inf) infinite |= 1u << i;
             if (FMT == KV_INT8) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) nan |= !(f[i][j] == f[i][j]);
@@ -388,7 +392,8 @@ __global__ void __launch_bounds__(PASSES == 2 ? 512 : 256, PASSES == 2 ? 1 : 2) 
                 float v[16];
                 RopeElem<__nv_bfloat16>::unpack(ra[i], *reinterpret_cast<float(*)[8]>(v));
                 RopeElem<__nv_bfloat16>::unpack(rb[i], *reinterpret_cast<float(*)[8]>(v + 8));
-                m = fmaxf(m, kv_amax(v));
+                bool inf;
+                m = fmaxf(m, kv_amax(v, inf));
             }
         }
         nan = FMT == KV_INT8 && (__hisnan(__low2bfloat16(seen)) || __hisnan(__high2bfloat16(seen)));
@@ -450,10 +455,11 @@ __global__ void __launch_bounds__(PASSES == 2 ? 512 : 256, PASSES == 2 ? 1 : 2) 
                 differ[k] = w[k] ^ kv_round4<FMT>(x[0], x[1], x[2], x[3]);
                 any |= differ[k];
             }
-            if (any) {
+            // an infinite member's interval is NaN, and so is its partner's: their bytes come from the formula too
+            if (any || infinite >> i & 1) {
                 const __nv_bfloat16* at = in + (long long)(r >> hshift) * ts + my_h * hs;
                 const unsigned long long p = position(r >> hshift);
-                unsigned todo = 0;  // pairs of which a byte differs
+                unsigned todo = infinite >> i & 1 ? 255u : 0u;  // pairs of which a byte differs
 #pragma unroll
                 for (int y = 0; y < 8; ++y) {
                     const int lo = INTER ? 2 * y : y, hi = INTER ? 2 * y + 1 : 8 + y;

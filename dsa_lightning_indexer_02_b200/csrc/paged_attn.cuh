@@ -16,7 +16,7 @@
 //   - q goes to fp16 after its head is scaled by a power of two to at most 2^14: no bit of bf16's is lost
 //     within 2^-28 of the head's largest.
 //   - V's scale 2^e * m, 1 <= m < 2, enters through the exponent: the softmax's reference is the running
-//     maximum of z + e, so that P = 2^(z + e - max) * m, rounded to fp16, keeps its bits however far the
+//     maximum of z + e (less 7), so that P = 2^(z + e - ref) * m, rounded to fp16, keeps its bits however far the
 //     scales of a row's pages lie apart; the row sum adds P's 2^-e part in fp32.
 //   - Rows are dealt to blocks by units, a row's units being its tiles and two more for its end: block c of
 //     C takes units [c, c + 1) * ceil(U / C) of all rows' U, in order, whatever the rows' lengths.  A row that
@@ -83,7 +83,12 @@ struct PagedCfg {
     static constexpr int Q_BYTES = NT == 2 ? 4 * 8 * 32 * 16 : 0;
     static constexpr int SMEM = RING_BYTES + META_BYTES + XCH_BYTES + Q_BYTES;
 };
-constexpr float kPagedNone = -1e30f;  // the running maximum before any key
+constexpr float kPagedNone = -1e30f;  // the reference before any key
+// The reference is taken kPagedBelow below the step's maximum, and moves when a logit exceeds it by kPagedMost (both in
+// log2): P * m stays below 2^15, under fp16's 2^16, and is right to 2^-11 of itself down to 2^-21 of the largest, below
+// to 2^-32 of the largest.  (Taken at the maximum, P is lost below 2^-25 of it: 16384 such keys of a warp beside one
+// large one were missing from the output altogether.)
+constexpr float kPagedBelow = 7.f, kPagedMost = 14.f;
 
 // Sequence and key count of row t; a bad one is reported and leaves the row empty.
 __device__ __forceinline__ void paged_row(const PagedParams& P, int t, int& b, int& n) {
@@ -648,15 +653,15 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
 #pragma unroll
                     for (int t = 1; t < KT; ++t) mx[x] = fmaxf(mx[x], fmaxf(z[t][nt][x], z[t][nt][2 + x]));
                 }
-                // the reference moves only when a logit exceeds it by more than 2^8
-                if (!started || __any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > 8.f)) {
+                // the reference moves only when a logit exceeds it by more than kPagedMost
+                if (!started || __any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > kPagedMost)) {
                     float alpha[2];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 4));
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 8));
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 16));
-                        const float up = !started || mx[x] > 8.f ? fmaxf(mx[x], kPagedNone) : 0.f;
+                        const float up = !started || mx[x] > kPagedMost ? fmaxf(mx[x] - kPagedBelow, kPagedNone) : 0.f;
                         alpha[x] = started ? ex2_approx(-up) : 1.f;  // at the start there is nothing to scale
                         m_run[nt][x] += up;
                         l_run[nt][x] *= alpha[x];

@@ -17,7 +17,9 @@
 //     within 2^-28 of the head's largest.
 //   - V's scale 2^e * m, 1 <= m < 2, enters through the exponent: the softmax's reference is the running
 //     maximum of z + e (less 7), so that P = 2^(z + e - ref) * m, rounded to fp16, keeps its bits however far the
-//     scales of a row's pages lie apart; the row sum adds P's 2^-e part in fp32.
+//     scales of a row's pages lie apart; the row sum adds P's 2^-e part in fp32.  Keys whose V scale lies 2^64 below
+//     that of the reference's, for which P alone may underflow, add theirs by an exponential of their own (all scales
+//     that an append makes are safe so; the test for it costs 0.5 to 1.5 % of the times below).
 //   - Rows are dealt to blocks by units, a row's units being its tiles and two more for its end: block c of
 //     C takes units [c, c + 1) * ceil(U / C) of all rows' U, in order, whatever the rows' lengths.  A row that
 //     one block holds whole is finished there; of the others each block writes its unnormalised part, and
@@ -90,6 +92,10 @@ constexpr float kPagedNone = -1e30f;  // the reference before any key
 // large one were missing from the output altogether.)
 constexpr float kPagedBelow = 7.f, kPagedMost = 14.f;
 
+// 2^(d / 2), d <= 0.  References differ by V's exponents too, up to 200 between pages, but the row sums behind them hold
+// that much: what is brought from one reference to another is multiplied by this twice, since 2^d alone may be 0.
+__device__ __forceinline__ float paged_root(float d) { return exp2f(0.5f * d); }
+
 // Sequence and key count of row t; a bad one is reported and leaves the row empty.
 __device__ __forceinline__ void paged_row(const PagedParams& P, int t, int& b, int& n) {
     b = P.seq ? P.seq[t] : t;
@@ -158,6 +164,14 @@ __device__ __forceinline__ void kv_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi)
         const __half2 r1 = __hsub2(*reinterpret_cast<const __half2*>(&m1), c);
         lo = *reinterpret_cast<const uint32_t*>(&r0), hi = *reinterpret_cast<const uint32_t*>(&r1);
     }
+}
+
+// A key whose logit plus e lies z above the reference adds P 2^-e, with P = 2^z and d = 2^-e, to the row sum: what of it
+// is missing from the product where P is below fp32's range.
+__device__ __forceinline__ float paged_missed(float z, float d) {
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(z + static_cast<float>(static_cast<int>(__float_as_uint(d) >> 23) - 127)));
+    return r - ex2_approx(z) * d;
 }
 
 // Where token `slot` of the pool starts: a product and sum in one step on the multipliers' side.
@@ -398,6 +412,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     uint32_t qf[NT == 1 ? 8 : 1][2];
     float qfac[NT][2];     // of heads nt * 8 + 2 j + {0, 1}: logits in log2 per unit of the product
     bool started = false;  // this warp has seen a key of the row: m_run holds maxima
+    float v_far;           // 2^-64 times the largest 2^e of the keys that the references were taken from
     float o[NT][8][4], m_run[NT][2], l_run[NT][2];
     int row = row0, left;  // left: tiles of the row still to come in this block
     bool whole;            // the block holds the row from its first tile to its last
@@ -419,6 +434,7 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
         whole = tile == 0 && left == nt;
         slot = now <= tile ? 0 : 1;
         started = false;
+        v_far = 0.f;
 #pragma unroll
         for (int nt8 = 0; nt8 < NT; ++nt8) {
             float f[8][4], top = 0.f;
@@ -508,8 +524,8 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
 #pragma unroll
         for (int p = 0; p < MOST; ++p) {
             if (p >= parts) continue;
-            const float wx = exp2f(t[p].x - m.x), wy = exp2f(t[p].y - m.y);
-            l.x += t[p].z * wx, l.y += t[p].w * wy;
+            const float hx = paged_root(t[p].x - m.x), hy = paged_root(t[p].y - m.y), wx = hx * hx, wy = hy * hy;
+            l.x += t[p].z * hx * hx, l.y += t[p].w * hy * hy;
             a[0] += v[p].x * wx, a[1] += v[p].y * wy, a[2] += v[p].z * wx, a[3] += v[p].w * wy;
         }
         const bool odd = g & 1;
@@ -609,6 +625,9 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
             }
             // logits in log2 plus V's exponent, less the reference; d = 2^-e, vm = V's scale * d
             float d[KT][2], vm[KT][2];
+            float v_least;  // the least V scale of the tiles, or this lane's of the step's 32 keys (0 where there is none)
+            if constexpr (IDX) v_least = fabsf(sc[32 + lane]);
+            else v_least = fminf(fabsf(sc[1]), fabsf(sc[3]));
 #pragma unroll
             for (int t = 0; t < KT; ++t) {
                 float ks[2], vs[2];
@@ -653,20 +672,45 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
 #pragma unroll
                     for (int t = 1; t < KT; ++t) mx[x] = fmaxf(mx[x], fmaxf(z[t][nt][x], z[t][nt][2 + x]));
                 }
-                // the reference moves only when a logit exceeds it by more than kPagedMost
-                if (!started || __any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > kPagedMost)) {
-                    float alpha[2];
+                // the reference moves only when a logit exceeds it by more than kPagedMost (and keys far below it are seen to)
+                if (!started || __any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > kPagedMost || v_least < v_far)) {
+                    float root[2], alpha[2];
+                    // the largest V scale of the step's keys, from one of which the reference may be taken (its power of two)
+                    float v_most, d_top = 0.f;
+                    if constexpr (IDX) {
+                        v_most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v_least)));
+                    } else {
+                        unsigned least = 0x7f800000u;
+#pragma unroll
+                        for (int t = 0; t < KT; ++t)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                d_top = fmaxf(d_top, d[t][y]);
+                                if (d[t][y] > 0.f) least = min(least, __float_as_uint(d[t][y]));
+                            }
+                        v_most = kv_pow2(127 - (int)(__reduce_min_sync(0xffffffffu, least) >> 23));
+                    }
+                    v_far = fmaxf(v_far, v_most * 5.421010862427522e-20f);  // 2^-64
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 4));
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 8));
                         mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 16));
                         const float up = !started || mx[x] > kPagedMost ? fmaxf(mx[x] - kPagedBelow, kPagedNone) : 0.f;
-                        alpha[x] = started ? ex2_approx(-up) : 1.f;  // at the start there is nothing to scale
+                        root[x] = started ? ex2_approx(-0.5f * up) : 1.f;  // at the start there is nothing to scale
+                        alpha[x] = root[x] * root[x];
                         m_run[nt][x] += up;
-                        l_run[nt][x] *= alpha[x];
+                        l_run[nt][x] = l_run[nt][x] * root[x] * root[x];
 #pragma unroll
                         for (int t = 0; t < KT; ++t) z[t][nt][x] -= up, z[t][nt][2 + x] -= up;
+                    }
+                    // P may be 0 for keys whose V scale is below v_far, though their weight is not: what the sum below misses
+                    if (IDX ? __any_sync(0xffffffffu, v_least < v_far) : d_top * v_far > 1.f) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int t = 0; t < KT; ++t)
+                                l_run[nt][x] += paged_missed(z[t][nt][x], d[t][0]) + paged_missed(z[t][nt][2 + x], d[t][1]);
                     }
 #pragma unroll
                     for (int dt = 0; dt < 8; ++dt) {
@@ -759,8 +803,9 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
             }
 #pragma unroll
             for (int p = 0; p < NSUB; ++p) {
-                w[p].x = exp2f(w[p].x - all[nt].x), w[p].y = exp2f(w[p].y - all[nt].y);
-                all[nt].z += w[p].z * w[p].x, all[nt].w += w[p].w * w[p].y;
+                const float hx = paged_root(w[p].x - all[nt].x), hy = paged_root(w[p].y - all[nt].y);
+                all[nt].z += w[p].z * hx * hx, all[nt].w += w[p].w * hy * hy;
+                w[p].x = hx * hx, w[p].y = hy * hy;
             }
 #pragma unroll
             for (int dt = 0; dt < 8; ++dt) {
@@ -835,8 +880,8 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const Pa
                 const float* src = at(p);
                 const float2 ml = *reinterpret_cast<const float2*>(src + kKvD);
                 const float4 v = *reinterpret_cast<const float4*>(src + lane * 4);
-                const float w = exp2f(ml.x - mx);
-                l += ml.y * w;
+                const float root = paged_root(ml.x - mx), w = root * root;
+                l += ml.y * root * root;
                 acc.x += v.x * w, acc.y += v.y * w, acc.z += v.z * w, acc.w += v.w * w;
             }
         }

@@ -337,14 +337,16 @@ dsa_status dsa_kv_append(const void *k_new, const void *v_new, int64_t k_ts, int
  *   out         bf16 [T, Hq, D];  lse  fp32 [T, Hq] natural-log sum-exp, or NULL
  * out, lse and ws must not overlap the inputs or one another.
  * A row without keys gets out = 0 and lse = -inf.  The cache, its scales and page_table as for
- * dsa_kv_append; any finite scales will do (those of dsa_kv_append are powers of two).  Only pages
- * that hold attended keys are read, and of those only attended tokens.
+ * dsa_kv_append; any other finite scales within the bounds below will do too (those of dsa_kv_append
+ * are powers of two), however far those of a row lie apart.  Only pages that hold attended keys are
+ * read, and of those only attended tokens.
  *   ws          device workspace of at least dsa_workspace_size(DSA_OP_PAGED_ATTN, L, T, Hq, HI, topk)
  *               bytes (which depends on Hq alone); one call at a time may use it
  * A row whose seq or n_keys is out of range counts as empty and a key whose page number is outside
  * [0, num_pages) is skipped; dsa_sync_status() reports both as DSA_ERR_DEVICE_INPUT.
  * Supported: D = 128, Hkv in {1, 2, 4}, Hq / Hkv <= 16, page_size in {16, 32, 64, 128}, topk <= 65536,
- * max_pages * page_size <= 2^30, num_pages * page_size < 2^31, scales up to 2^120 in size.
+ * max_pages * page_size <= 2^30, num_pages * page_size < 2^31, K scales up to 2^120 in size, V scales of 0 or 2^-80
+ * to 2^120 in size (values of smaller ones lose bits; their keys' weights do not).
  */
 dsa_status dsa_paged_attn(const void *q, const void *k_pages, const void *v_pages, const float *k_scale,
                           const float *v_scale, const int32_t *page_table, const int32_t *seq, const int32_t *n_keys,

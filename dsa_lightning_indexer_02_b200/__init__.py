@@ -138,13 +138,27 @@ def _ptr(t):
 _fast = None
 
 
+class _Ctypes:
+    """Stands in for the marshalling module: declines every call, which is then made through ctypes."""
+    rope = kv_append = paged_attn = staticmethod(lambda *operands: None)
+
+
 def _native():
     """The marshalling module: the checks below and the C call in one step, for operands that need no error
-    message (None otherwise).  Loaded with the first call that uses it, since it needs torch."""
+    message (None otherwise).  Loaded with the first call that uses it, since it needs torch; where it was not
+    built for this interpreter and torch, calls go through ctypes, with a warning."""
     global _fast
-    import torch  # noqa: F401
-    from . import _marshal
-    _fast = _marshal
+    import importlib.util
+    import warnings
+    from . import build
+    path = build.marshal_path()
+    try:
+        spec = importlib.util.spec_from_file_location(__name__ + "._marshal", path)
+        _fast = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_fast)
+    except ImportError as e:
+        warnings.warn(f"{path} is not built ({e}): calls go through ctypes, some 10 us slower each", RuntimeWarning)
+        _fast = _Ctypes
     return _fast
 
 

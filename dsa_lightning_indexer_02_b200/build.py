@@ -1,5 +1,10 @@
-"""Build libdsa.so (sm_100a) in-tree with nvcc, and with the host compiler the binding's marshalling module
-_marshal.so, which links it.  No GPU is needed to build."""
+"""Build libdsa.so (sm_100a) in-tree with nvcc, and with the host compiler the binding's marshalling module, which
+links it.  No GPU is needed to build.
+
+build_lib() makes the library alone, for C callers: nvcc is all it needs.  build() adds the module, which needs the
+headers of the running interpreter and of torch; without it the binding makes its calls through ctypes, slower by
+some 10 us each.
+"""
 from __future__ import annotations
 
 import os
@@ -16,7 +21,6 @@ DEPS = [os.path.join(HERE, "csrc", f) for f in (
 DEPS += [os.path.join(ROOT, "include", "dsa.h"), os.path.abspath(__file__)]
 
 MARSHAL_SRC = os.path.join(HERE, "csrc", "marshal.cpp")
-MARSHAL = os.path.join(HERE, "_marshal.so")
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v", "--expt-relaxed-constexpr"]
@@ -36,35 +40,55 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in DEPS)
 
 
-def build_marshal(force: bool = False) -> str:
-    """The marshalling module, against the running interpreter's and torch's headers."""
-    deps = (MARSHAL_SRC, os.path.join(ROOT, "include", "dsa.h"))
-    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(d) <= os.path.getmtime(MARSHAL) for d in deps):
-        return MARSHAL
+def marshal_path() -> str:
+    """Where the marshalling module for the running interpreter and torch lies.  It is compiled against the inline
+    code of both, so its name holds what must agree: a module of others is never loaded, and theirs is built anew."""
     import sysconfig
     import torch
+    abi = f"{sysconfig.get_config_var('SOABI')}-torch-{torch.__version__}-{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(HERE, f"_marshal.{abi}.so")
+
+
+def build_marshal(force: bool = False) -> str | None:
+    """The marshalling module; None, with a message, where torch or the host compiler is missing."""
+    try:
+        import torch
+        out = marshal_path()
+    except ImportError as e:
+        sys.stderr.write(f"marshalling module not built: {e}\n")
+        return None
+    deps = (MARSHAL_SRC, os.path.join(ROOT, "include", "dsa.h"), os.path.abspath(__file__))
+    if not force and os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps):
+        return out
+    import sysconfig
     top = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", os.path.join(ROOT, "include"), "-I", sysconfig.get_paths()["include"], "-isystem", f"{top}/include",
            "-isystem", f"{top}/include/torch/csrc/api/include", "-isystem", f"{cuda}/include", MARSHAL_SRC,
-           "-o", MARSHAL + ".tmp", LIB, f"-L{top}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-o", out + ".tmp", LIB, f"-L{top}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{top}/lib"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+    except FileNotFoundError as e:
+        sys.stderr.write(f"marshalling module not built: {e}\n")
+        return None
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("the host compiler failed building _marshal.so")
-    os.replace(MARSHAL + ".tmp", MARSHAL)
-    return MARSHAL
+        raise RuntimeError("the host compiler failed building the marshalling module")
+    os.replace(out + ".tmp", out)
+    return out
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """The library and the marshalling module."""
     lib = build_lib(force, verbose)
     build_marshal(force)
     return lib
 
 
 def build_lib(force: bool = False, verbose: bool = False) -> str:
+    """libdsa.so alone, whose interface is include/dsa.h."""
     if not force and up_to_date():
         return LIB
     cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), SRC, "-Xlinker", "-soname=libdsa.so", "-o", LIB + ".tmp"]

@@ -3,9 +3,9 @@
 // over all its n_keys[t] cached keys, or over those that idx names; ks, vs are the scales of the key's page.
 //
 // Bound by the cache's bytes: at 32 query and 4 KV heads a key is 1 KB against 16 Kflop.
-//   - A warp works alone: it owns one KV head and 16 keys of every tile, copies their K and V rows
-//     (16 x 128 bytes each) and scales into a ring of its own with cp.async and multiplies them, so
-//     that no barrier stands between copies and products and every SM keeps 16 rings in flight.
+//   - A warp works alone: it owns one KV head and 32 keys of every tile, copies their K and V rows
+//     (32 x 128 bytes each) and scales into a ring of its own with cp.async and multiplies them, so
+//     that no barrier stands between copies and products and every SM keeps 12 rings in flight.
 //     Dense rows and selected keys differ only in where a lane's key number comes from.
 //   - Both products run on fp16 matrix instructions, where e4m3 and int8 values are exact:
 //     S^T[keys x heads] = K Q^T and O^T += V^T P^T, the G query heads of the KV head as columns.  The rows of
@@ -46,7 +46,7 @@ namespace dsa {
 
 constexpr int kPagedPartCtas = 296;     // most blocks that share rows; each has two partial slots
 constexpr int kPagedSharedRows = 1184;  // most rows that are dealt by units
-constexpr int kPagedMostCluster = 8;    // most blocks of a cluster (the most that any device takes)
+constexpr int kPagedMostCluster = 8;    // most blocks of a cluster (the portable limit)
 constexpr int kPagedPartStride = kKvD + 4;  // floats of a partial: O[128], max, sum, 2 pad
 constexpr int kPagedRowTiles = 2;       // what the end of a row costs a block, in tiles, when rows are dealt
 
@@ -67,7 +67,7 @@ struct PagedParams {
     long long* row_start;              // [T + 1]: where the rows start, in units dealt; behind them a block's units
 };
 
-// NT: groups of 8 query heads of a KV head.  KT: 16-key tiles of a warp's step.
+// NT: groups of 8 query heads of a KV head.  KT: 16-key tiles of a warp's step (a transposed load of V takes two).
 template <int NT>
 struct PagedCfg {
     static constexpr int KT = 2;
@@ -182,7 +182,7 @@ __device__ __forceinline__ const uint8_t* paged_token(const uint8_t* base, uint3
     return at;
 }
 
-// IDX: keys named by idx; otherwise a step's 16 keys lie side by side in one page.  CLU: P.cluster blocks a row.
+// IDX: keys named by idx; otherwise the 16 keys of a step's tile lie side by side in one page.  CLU: P.cluster blocks a row.
 template <int FMT, int NT, int HKV, bool IDX, bool CLU>
 __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) paged_attn_kernel(const PagedParams P) {
     using C = PagedCfg<NT>;
@@ -298,13 +298,13 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
     uint4* q_sh = reinterpret_cast<uint4*>(smem + C::RING_BYTES + C::META_BYTES + C::XCH_BYTES) + head * (8 * 32) + lane;
 
     // ---- copies.  A step's keys pass three stages, one iteration apart: their numbers are loaded, their
-    // pages looked up, their rows copied.  With IDX lane i has key i of the step (KT = 1: i mod 16);
+    // pages looked up, their rows copied.  With IDX lane i has key i of the step;
     // otherwise lane i has the first key of 16-key tile i mod 16, for i mod 16 < KT.
     int f_row = row0, f_tile = tile0, f_b, f_n;  // front cursor: the next tile whose keys are loaded
     int f_at = now;
     paged_row(P, f_row, f_b, f_n);
     int f_nt = (paged_count(P, f_n) + TK - 1) / TK;
-    const int my_key = IDX ? (KT == 2 ? lane : lane & 15) : (lane & 15) * 16;
+    const int my_key = IDX ? lane : (lane & 15) * 16;
     const bool has_key = IDX || (lane & 15) < KT;
     int a_key = -1, a_n = 0, a_b = 0;   // numbers loaded
     int b_key = -1, b_n = 0, b_pid = 0; // pages looked up; nothing waits for the page number before the copy
@@ -374,12 +374,8 @@ __global__ void __launch_bounds__(PagedCfg<NT>::THREADS, PagedCfg<NT>::CTAS) pag
                 }
                 const bool ok = b_slot >= 0;
                 const long long at = ok ? (long long)(b_slot >> P.page_shift) * HKV + head : 0;
-                if (KT == 2) {
-                    cp_async_4(sc + lane, P.k_scale + at, ok);
-                    cp_async_4(sc + 32 + lane, P.v_scale + at, ok);
-                } else {
-                    cp_async_4(sc + (lane & 15) + (lane & 16) * 2, (lane < 16 ? P.k_scale : P.v_scale) + at, ok);
-                }
+                cp_async_4(sc + lane, P.k_scale + at, ok);
+                cp_async_4(sc + 32 + lane, P.v_scale + at, ok);
             }
         } else {
             int s[KT], n[KT], all = 0;

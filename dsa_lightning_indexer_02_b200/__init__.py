@@ -87,6 +87,7 @@ _SIGS = {
     "dsa_error_site": (ctypes.c_uint, []),
     "dsa_profile_begin": (None, []),
     "dsa_profile_end": (_i, [_p, _p]),
+    "dsa_profile_end_kinds": (_i, [_i, _p, _p]),
     "dsa_launch_count": (_i64, []),
     "dsa_read_counters": (_i, [_p, _i, _i]),
     "dsa_selftest_timeout": (_i, [_i64, _p]),
@@ -534,7 +535,7 @@ def profile_begin() -> None:
 def profile_end() -> dict:
     launches = (ctypes.c_int64 * len(PROFILE_KINDS))()
     ms = (ctypes.c_double * len(PROFILE_KINDS))()
-    _check(_lib.dsa_profile_end(launches, ms), "dsa_profile_end")
+    _check(_lib.dsa_profile_end_kinds(len(PROFILE_KINDS), launches, ms), "dsa_profile_end")
     return {k: {"launches": int(launches[i]), "ms": float(ms[i])} for i, k in enumerate(PROFILE_KINDS)}
 
 

@@ -80,6 +80,7 @@ struct LaunchScope {
 
 enum { K_INDEX = 0, K_TOPK = 1, K_ATTN = 2, K_COMBINE = 3, K_APPEND = 4, K_ADVANCE = 5, K_SELFTEST = 6, K_KL = 7, K_ROPE = 8,
        K_KV_APPEND = 9, K_PAGED_ATTN = 10 };
+static_assert(K_PAGED_ATTN == DSA_PROFILE_ALL_KINDS - 1, "the header tells all kinds");
 
 dsa_status launch_status() {
     cudaError_t e = cudaGetLastError();
@@ -1289,10 +1290,15 @@ void dsa_profile_begin(void) {
 }
 
 dsa_status dsa_profile_end(int64_t* launches, double* total_ms) {
+    return dsa_profile_end_kinds(DSA_PROFILE_KINDS, launches, total_ms);
+}
+
+dsa_status dsa_profile_end_kinds(int kinds, int64_t* launches, double* total_ms) {
+    if (kinds < 0) return DSA_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> lk(g_prof_mu);
     g_prof_on = false;
     dsa_status st = DSA_OK;
-    for (int i = 0; i < DSA_PROFILE_KINDS; ++i) {
+    for (int i = 0; i < kinds; ++i) {
         if (launches) launches[i] = 0;
         if (total_ms) total_ms[i] = 0.0;
     }
@@ -1302,6 +1308,7 @@ dsa_status dsa_profile_end(int64_t* launches, double* total_ms) {
             st = DSA_ERR_CUDA;
             continue;
         }
+        if (r.kind >= kinds) continue;
         if (launches) launches[r.kind] += 1;
         if (total_ms) total_ms[r.kind] += ms;
     }

@@ -385,11 +385,15 @@ unsigned int dsa_error_site(void);
  * milliseconds.  Kinds: 0 indexer, 1 top-k, 2 sparse attention, 3 split combine, 4 decode
  * append and 5 context advance (both now done inside other kernels: always 0), 6 self-test,
  * 7 indexer warm-up KL, 8 rotary positions, 9 paged-cache append, 10 paged-cache attention (its
- * merge of splits counts under 3).  Arrays have DSA_PROFILE_KINDS entries.
+ * merge of splits counts under 3).  dsa_profile_end() fills arrays of DSA_PROFILE_KINDS entries, the
+ * kinds before 8, whose number never changes; dsa_profile_end_kinds() does the same for the first
+ * `kinds` of all (entries beyond those that the library knows are 0).  An array may be NULL.
  */
-#define DSA_PROFILE_KINDS 11
+#define DSA_PROFILE_KINDS 8
+#define DSA_PROFILE_ALL_KINDS 11
 void dsa_profile_begin(void);
 dsa_status dsa_profile_end(int64_t *launches, double *total_ms);
+dsa_status dsa_profile_end_kinds(int kinds, int64_t *launches, double *total_ms);
 
 /*
  * Diagnostic path counters, accumulated on the device since load or the last reset:

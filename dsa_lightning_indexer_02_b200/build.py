@@ -105,5 +105,5 @@ def build_lib(force: bool = False, verbose: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    build(force="--force" in sys.argv, verbose=True)
+    (build_lib if "--lib" in sys.argv else build)(force="--force" in sys.argv, verbose=True)
     print(LIB)

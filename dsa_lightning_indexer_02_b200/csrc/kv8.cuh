@@ -23,7 +23,7 @@
 //
 // Measured: 16 single tokens, 4 KV heads 4.1 us, a launch and two dependent loads more than an empty kernel's 2.2; 61
 // chunks of up to 37 tokens, int8 3.4 us; 23 K tokens of 8 sequences 23.6 us, where the bytes alone take 11: bound by
-// instructions (issue slots 57 % busy, two blocks of 256 threads an SM): by count of operations a third of a key
+// instructions (issue slots 55 % busy, two blocks of 256 threads an SM): by count of operations a third of a key
 // block's make sines, which its two heads share, and a fifth round twice.
 #pragma once
 

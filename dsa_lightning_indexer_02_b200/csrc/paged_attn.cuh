@@ -19,7 +19,7 @@
 //     maximum of z + e (less 7), so that P = 2^(z + e - ref) * m, rounded to fp16, keeps its bits however far the
 //     scales of a row's pages lie apart; the row sum adds P's 2^-e part in fp32.  Keys whose V scale lies 2^64 below
 //     that of the reference's, for which P alone may underflow, add theirs by an exponential of their own (all scales
-//     that an append makes are safe so; the test for it costs 0.5 to 1.5 % of the times below).
+//     that an append makes are safe so; the test for it costs 1 to 2 % of the times below).
 //   - Rows are dealt to blocks by units, a row's units being its tiles and two more for its end: block c of
 //     C takes units [c, c + 1) * ceil(U / C) of all rows' U, in order, whatever the rows' lengths.  A row that
 //     one block holds whole is finished there; of the others each block writes its unnormalised part, and
@@ -29,13 +29,13 @@
 //     through each other's shared memory.
 //
 // Measured (32 query heads):
-//   16 x 131328 keys, 4 KV heads, e4m3   317-336 us, 6.3-6.7 TB/s, 98-104 % of the copy rate: bound by memory
-//   122 rows of 1 to 16000 keys, 2 KV heads, int8   74 us, 2.2 TB/s: bound by instructions and their latencies (16 heads a
+//   16 x 131328 keys, 4 KV heads, e4m3   328-341 us, 6.3-6.5 TB/s, 97-101 % of the copy rate: bound by memory
+//   122 rows of 1 to 16000 keys, 2 KV heads, int8   75 us, 2.2 TB/s: bound by instructions and their latencies (16 heads a
 //                                        KV head; issue slots 55 % busy with 3 warps a scheduler)
-//   1024 rows x 2048 of 32768 keys       253 us, 8.5 TB/s of gathered rows, from L2: the same (56 %, 560 instructions
+//   1024 rows x 2048 of 32768 keys       257 us, 8.4 TB/s of gathered rows, from L2: the same (57 %, 570 instructions
 //                                        for a warp's 32 keys; leaving out V's conversions alone saves 3 %)
-//   16 rows x 2048 of 131328 keys        13.3 us (5.3 for the bytes): latency of launch, look-up, four tiles, join
-//   1 row of 777 keys                    8.9 us: latency of launch, look-up, two tiles, join
+//   16 rows x 2048 of 131328 keys        13.5 us (5.3 for the bytes): latency of launch, look-up, four tiles, join
+//   1 row of 777 keys                    9.2 us: latency of launch, look-up, two tiles, join
 #pragma once
 
 #include <type_traits>

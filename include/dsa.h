@@ -339,7 +339,9 @@ dsa_status dsa_kv_append(const void *k_new, const void *v_new, int64_t k_ts, int
  * A row without keys gets out = 0 and lse = -inf.  The cache, its scales and page_table as for
  * dsa_kv_append; any other finite scales within the bounds below will do too (those of dsa_kv_append
  * are powers of two), however far those of a row lie apart.  Only pages that hold attended keys are
- * read, and of those only attended tokens.
+ * read, and of those only attended tokens.  How rows are spread over the GPU is chosen by the most
+ * that one can hold, max_pages * page_size or topk: a table much wider than its sequences is served
+ * as if they were long, slower by a third or so if they are short.
  *   ws          device workspace of at least dsa_workspace_size(DSA_OP_PAGED_ATTN, L, T, Hq, HI, topk)
  *               bytes (which depends on Hq alone); one call at a time may use it
  * A row whose seq or n_keys is out of range counts as empty and a key whose page number is outside

@@ -57,7 +57,8 @@ def test_bytes_next_to_a_tie(cuda_ok, fmt, inter, form):
     assert np.all((got[i, two] == want2) | (got[i, two] == lo) | (got[i, two] == hi))
 
 
-@pytest.mark.parametrize("R,off,inter", [(128, 0, False), (64, 32, True)], ids=["half", "interleaved"])
+@pytest.mark.parametrize("R,off,inter", [(128, 0, False), (64, 32, True), (48, 40, False), (112, 8, True), (16, 112, False),
+                                         (80, 48, True)])
 @pytest.mark.parametrize("page,Hkv,fmt", [(64, 4, E4M3), (16, 2, INT8), (128, 1, E4M3)])
 def test_bytes_of_random_keys(cuda_ok, page, Hkv, fmt, R, off, inter):
     """Every byte of ordinary keys is the exact product's.  The angle's own error (2^-52 of its size: the frequency's
